@@ -14,6 +14,7 @@ _p = ctypes.c_void_p
 _i = ctypes.c_int
 _f = ctypes.c_float
 _sz = ctypes.c_size_t
+_ll = ctypes.c_longlong
 
 # name -> (restype, argtypes), mirroring include/cgtp.h
 SIGNATURES = {
@@ -52,6 +53,17 @@ SIGNATURES = {
     "cgtp_tp_backward_noalloc": (_i, [_p, _i, _p, _p, _p, _p, _p, _p, _p, _p]),
     "cgtp_cp_forward": (_i, [_p, _i, _i, _p, _p, _p, _p, _p, _p, _p]),
     "cgtp_cp_backward_workspace_size": (_i, [_p, _i, _i, ctypes.POINTER(_sz)]),
+    "cgtp_token_sort_workspace_size": (_i, [_i, _i, ctypes.POINTER(_sz)]),
+    "cgtp_token_sort": (_i, [_i, _i, _p, _p, _p, _p, _sz, _p]),
+    "cgtp_embed_forward": (_i, [_i, _i, _i, _p, _p, _f, _p, _ll, _p]),
+    "cgtp_embed_backward_workspace_size": (_i, [_i, _i, ctypes.POINTER(_sz)]),
+    "cgtp_embed_backward": (_i, [_i, _i, _i, _p, _p, _p, _ll, _f, _p, _p, _sz, _p]),
+    "cgtp_group_norm_workspace_size": (_i, [_i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "cgtp_group_norm_forward": (_i, [_i, _i, _i, _i, _p, _i, _p, _ll, _p, _p, _f, _i, _p, _ll, _p, _p, _p, _sz, _p]),
+    "cgtp_group_norm_backward": (_i, [_i, _i, _i, _i, _p, _i, _p, _ll, _p, _p, _p, _p, _i, _p, _ll, _p, _ll, _p, _p,
+                                      _p, _sz, _p]),
+    "cgtp_orthogonalise_workspace_size": (_i, [_i, _i, _i, ctypes.POINTER(_sz)]),
+    "cgtp_orthogonalise": (_i, [_i, _i, _i, _i, _f, _p, _p, _p, _sz, _p]),
     "cgtp_cp_backward": (_i, [_p, _i, _i, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _p, _sz, _p]),
 }
 

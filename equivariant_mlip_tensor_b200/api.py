@@ -157,6 +157,221 @@ def scatter_add_rows(idx, src, dst):
     return dst
 
 
+# ------------------------------------------------------------ training-side operators
+# These run on the device of their tensors, on that device's current stream.
+def _same_device(first, **others):
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+
+
+def _check_rows(t, name, n=None, width=None):
+    """A [n][width] fp32 tensor whose rows are contiguous (any row stride, as
+    x[:, 0, :] of features [n][(lmax+1)^2][width] has); returns the stride."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype != torch.float32:
+        raise ValueError(f"{name} must be {torch.float32}, got {t.dtype}")
+    if t.dim() != 2 or (n is not None and t.shape[0] != n) or (width is not None and t.shape[1] != width):
+        raise ValueError(f"{name} must be [{'n' if n is None else n}][{'width' if width is None else width}], "
+                         f"got {tuple(t.shape)}")
+    n, width = t.shape
+    stride = t.stride(0) if n > 1 else max(width, t.stride(0))
+    if (width > 1 and t.stride(1) != 1) or stride < width:
+        raise ValueError(f"{name} must have contiguous rows that do not overlap, got strides {t.stride()}")
+    return stride
+
+
+def _check_vector(t, dtype, name, size):
+    _check(t, dtype, name)
+    if t is not None and (t.dim() != 1 or t.numel() != size):
+        raise ValueError(f"{name} must have {size} elements, got {tuple(t.shape)}")
+
+
+def _call_on(dev, name, *args):
+    """Call an entry point on the tensors' device and that device's current stream."""
+    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    if dev.index == torch.cuda.current_device():
+        call(name, *args, stream)
+    else:
+        with torch.cuda.device(dev):
+            call(name, *args, stream)
+
+
+def _workspace(workspace, need, dev):
+    """(tensor, bytes): the caller's workspace, or one of the size asked for."""
+    if workspace is None:
+        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev), need
+    if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != dev:
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _bytes(name, *args):
+    b = ctypes.c_size_t()
+    call(name, *args, ctypes.byref(b))
+    return b.value
+
+
+@dataclass
+class TokenOrder:
+    """Tokens sorted once for every gradient of a batch (cgtp_token_sort)."""
+    n_rows: int
+    order: torch.Tensor   # [n] int32, the position each sorted token came from
+    sorted: torch.Tensor  # [n] int32, ascending; n_rows for tokens outside [0, n_rows)
+
+
+def token_sort_workspace_bytes(n, n_rows):
+    return _bytes("cgtp_token_sort_workspace_size", n, n_rows)
+
+
+def token_sort(tokens, n_rows, workspace=None):
+    """Stable sort of tokens [n] into [0, n_rows) for embed_backward."""
+    _check(tokens, torch.int32, "tokens")
+    n, dev = tokens.numel(), tokens.device
+    order, srt = torch.empty((2, n), dtype=torch.int32, device=dev)
+    ws, nb = _workspace(workspace, token_sort_workspace_bytes(n, n_rows), dev)
+    _call_on(dev, "cgtp_token_sort", n, n_rows, _ptr(tokens), _ptr(order), _ptr(srt), _ptr(ws), nb)
+    return TokenOrder(n_rows, order, srt)
+
+
+def embed_forward(tokens, table, scale=1.0, out=None):
+    """out[k] = scale * table[tokens[k]]; a zero row for a token outside the table.
+
+    out: [n][width], possibly with a row stride (x[:, 0, :] of features)."""
+    _check(tokens, torch.int32, "tokens")
+    _check(table, torch.float32, "table")
+    if table.dim() != 2:
+        raise ValueError(f"table must be [n_rows][width], got {tuple(table.shape)}")
+    n, (n_rows, width) = tokens.numel(), table.shape
+    if out is None:
+        out = torch.empty((n, width), dtype=torch.float32, device=table.device)
+    stride = _check_rows(out, "out", n, width)
+    _same_device(table, tokens=tokens, out=out)
+    _call_on(table.device, "cgtp_embed_forward", n, n_rows, width, _ptr(tokens), _ptr(table), float(scale), _ptr(out), stride)
+    return out
+
+
+def embed_backward_workspace_bytes(n, width):
+    return _bytes("cgtp_embed_backward_workspace_size", n, width)
+
+
+def embed_backward(order, grad_out, scale=1.0, out=None, workspace=None):
+    """grad_table [n_rows][width] of embed_forward for the tokens that order
+    (token_sort) holds; grad_out [n][width], possibly with a row stride."""
+    n = order.order.numel()
+    stride = _check_rows(grad_out, "grad_out", n)
+    _check_vector(order.order, torch.int32, "order", n)
+    _check_vector(order.sorted, torch.int32, "sorted", n)
+    width, dev = grad_out.shape[1], grad_out.device
+    if out is None:
+        out = torch.empty((order.n_rows, width), dtype=torch.float32, device=dev)
+    _check(out, torch.float32, "out")
+    if tuple(out.shape) != (order.n_rows, width):
+        raise ValueError(f"out must be [{order.n_rows}][{width}], got {tuple(out.shape)}")
+    _same_device(grad_out, order=order.order, sorted=order.sorted, out=out)
+    ws, nb = _workspace(workspace, embed_backward_workspace_bytes(n, width), dev)
+    _call_on(dev, "cgtp_embed_backward", n, order.n_rows, width, _ptr(order.order), _ptr(order.sorted), _ptr(grad_out),
+             stride, float(scale), _ptr(out), _ptr(ws), nb)
+    return out
+
+
+# activations of the group norm (cgtp_act)
+ACTIVATIONS = {None: 0, "silu": 1}
+
+
+def group_norm_workspace_bytes(n, n_samples, channels, groups):
+    return _bytes("cgtp_group_norm_workspace_size", n, n_samples, channels, groups)
+
+
+def _norm_shape(x, gamma, beta, groups, graph_ptr, activation):
+    stride = _check_rows(x, "x")
+    n, c = x.shape
+    _check_vector(gamma, torch.float32, "gamma", c)
+    _check_vector(beta, torch.float32, "beta", c)
+    _check(graph_ptr, torch.int32, "graph_ptr")
+    if activation not in ACTIVATIONS:
+        raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
+    if groups < 1 or c % groups:
+        raise ValueError(f"{c} channels cannot be cut into {groups} equal groups")
+    if graph_ptr is not None and graph_ptr.numel() < 1:
+        raise ValueError("graph_ptr must hold n_samples + 1 offsets")
+    return n, c, 1 if graph_ptr is None else graph_ptr.numel() - 1, stride
+
+
+def group_norm_forward(x, gamma, beta, groups, graph_ptr=None, eps=1e-5, activation=None, max_rows=0, out=None,
+                       workspace=None):
+    """Per-graph group norm of scalar features x [n][channels] (possibly with a
+    row stride: x[:, 0, :]), then gamma, beta (nullable) and the activation
+    (None or "silu").  Returns (y, mean, rstd), the statistics [samples][groups].
+
+    max_rows: a bound on the rows of a graph where it is known (0: unknown).
+    Rows of out that belong to no graph are left as they were."""
+    n, c, b, stride = _norm_shape(x, gamma, beta, groups, graph_ptr, activation)
+    dev = x.device
+    if out is None:
+        out = torch.empty((n, c), dtype=torch.float32, device=dev)
+    out_stride = _check_rows(out, "out", n, c)
+    _same_device(x, gamma=gamma, beta=beta, graph_ptr=graph_ptr, out=out)
+    mean, rstd = torch.empty((2, b, groups), dtype=torch.float32, device=dev)
+    ws, nb = _workspace(workspace, group_norm_workspace_bytes(n, b, c, groups), dev)
+    _call_on(dev, "cgtp_group_norm_forward", n, b, c, groups, _ptr(graph_ptr), max_rows, _ptr(x), stride, _ptr(gamma),
+             _ptr(beta), float(eps), ACTIVATIONS[activation], _ptr(out), out_stride, _ptr(mean), _ptr(rstd), _ptr(ws), nb)
+    return out, mean, rstd
+
+
+def group_norm_backward(x, gamma, beta, groups, mean, rstd, grad_y, graph_ptr=None, activation=None, max_rows=0,
+                        want_x=True, want_params=True, grad_x=None, workspace=None):
+    """Adjoint of group_norm_forward: (grad_x, grad_gamma, grad_beta); the
+    unrequested ones are None.  Rows of grad_x that belong to no graph are left
+    as they were."""
+    n, c, b, stride = _norm_shape(x, gamma, beta, groups, graph_ptr, activation)
+    dev = x.device
+    gy_stride = _check_rows(grad_y, "grad_y", n, c)
+    for t, nm in ((mean, "mean"), (rstd, "rstd")):
+        _check(t, torch.float32, nm)
+        if t.numel() != b * groups:
+            raise ValueError(f"{nm} must be [{b}][{groups}], got {tuple(t.shape)}")
+    gx_stride = 0
+    if want_x:
+        if grad_x is None:
+            grad_x = torch.empty((n, c), dtype=torch.float32, device=dev)
+        gx_stride = _check_rows(grad_x, "grad_x", n, c)
+    else:
+        grad_x = None
+    _same_device(x, gamma=gamma, beta=beta, graph_ptr=graph_ptr, mean=mean, rstd=rstd, grad_y=grad_y, grad_x=grad_x)
+    gg, gb = torch.empty((2, c), dtype=torch.float32, device=dev) if want_params else (None, None)
+    ws, nb = _workspace(workspace, group_norm_workspace_bytes(n, b, c, groups), dev)
+    _call_on(dev, "cgtp_group_norm_backward", n, b, c, groups, _ptr(graph_ptr), max_rows, _ptr(x), stride, _ptr(gamma),
+             _ptr(beta), _ptr(mean), _ptr(rstd), ACTIVATIONS[activation], _ptr(grad_y), gy_stride, _ptr(grad_x), gx_stride,
+             _ptr(gg), _ptr(gb), _ptr(ws), nb)
+    return grad_x, gg, gb
+
+
+def orthogonalise_workspace_bytes(batch, rows, cols):
+    return _bytes("cgtp_orthogonalise_workspace_size", batch, rows, cols)
+
+
+def orthogonalise(update, steps=5, scale=1.0, out=None, workspace=None):
+    """scale * (near-)orthogonal factor of each matrix of update [..., rows, cols]
+    by Newton-Schulz products (cgtp_orthogonalise); out may be update."""
+    _check(update, torch.float32, "update")
+    if update.dim() < 2:
+        raise ValueError(f"update must be [..., rows, cols], got {tuple(update.shape)}")
+    rows, cols = update.shape[-2:]
+    batch = int(np.prod(update.shape[:-2]))
+    if out is None:
+        out = torch.empty_like(update)
+    _check(out, torch.float32, "out")
+    if out.shape != update.shape:
+        raise ValueError(f"out must have the shape of update, got {tuple(out.shape)}")
+    _same_device(update, out=out)
+    ws, nb = _workspace(workspace, orthogonalise_workspace_bytes(batch, rows, cols), update.device)
+    _call_on(update.device, "cgtp_orthogonalise", batch, rows, cols, steps, float(scale), _ptr(update), _ptr(out), _ptr(ws),
+             nb)
+    return out
+
+
 class Plan:
     """Paths and CG coefficients of one irreps shape (lmax_in, lmax_sh, lmax_out, mult).
 

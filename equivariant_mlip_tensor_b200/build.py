@@ -35,7 +35,8 @@ NVCC_FLAGS = BASE_FLAGS + ["-lineinfo"]
 # variants for the shapes of CGTP_VARIANT_CONFIGS
 PER_SHAPE = ["conv_fwd.cu", "conv_bwd.cu", "conv_dd.cu", "tp.cu", "cp.cu"]
 PER_VARIANT_SHAPE = ["conv_paths.cu", "conv_shared.cu"]
-SHAPE_FREE = ["graph.cu", "radial.cu", "misc.cu", "abi.cu", "cg_table.cpp", "uvw.cu", "lanes.cu"]
+SHAPE_FREE = ["graph.cu", "radial.cu", "misc.cu", "abi.cu", "cg_table.cpp", "uvw.cu", "lanes.cu",
+              "embed.cu", "norm.cu", "ortho.cu"]
 
 
 def cutlass_include():

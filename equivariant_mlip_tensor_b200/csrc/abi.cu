@@ -11,6 +11,7 @@
 #include "configs.h"
 #include "launch.h"
 #include "structure.h"
+#include "train_ops.h"
 #include "../../include/cgtp.h"
 
 namespace cgtp {
@@ -1050,3 +1051,175 @@ extern "C" cgtp_status cgtp_tp_backward_noalloc(cgtp_plan p, int batch, const fl
   CGTP_CONFIGS(CGTP_TPB_NOALLOC_ENTRY)
   return e == cudaSuccess ? CGTP_OK : cuda_fail(e);
 }
+
+// ---------------------------------------------------------------------------
+// Training-side operators: embedding, group norm, orthogonalised updates.
+// They use no coefficient table, so a first call may be inside a stream
+// capture.
+namespace {
+
+constexpr int kMaxTokens = 1 << 30;
+
+bool aligned256(const void* p) { return ((uintptr_t)p & 255u) == 0; }
+
+// Rows of `width` floats, `stride` apart: both in range, and every offset in 64 bits.
+bool rows_ok(const void* p, long long n, long long width, long long stride) {
+  return n == 0 || width == 0 || (p != nullptr && stride >= width && stride <= (1LL << 40));
+}
+
+cgtp_status workspace_ok(const void* ws, size_t have, size_t need) {
+  if (need > 0 && (ws == nullptr || have < need)) return CGTP_ERR_WORKSPACE;
+  return need > 0 && !aligned256(ws) ? CGTP_ERR_INVALID_ARG : CGTP_OK;
+}
+
+cgtp_status launched(cudaError_t e) { return e == cudaSuccess ? CGTP_OK : cuda_fail(e); }
+
+}  // namespace
+
+extern "C" {
+
+cgtp_status cgtp_token_sort_workspace_size(int n, int n_rows, size_t* bytes) {
+  if (n < 0 || n > kMaxTokens || n_rows < 0 || bytes == nullptr) return CGTP_ERR_INVALID_ARG;
+  *bytes = n == 0 ? 0 : token_sort_workspace(n, n_rows);
+  return CGTP_OK;
+}
+
+cgtp_status cgtp_token_sort(int n, int n_rows, const int* tokens, int* order, int* sorted, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  if (cgtp_token_sort_workspace_size(n, n_rows, &need) != CGTP_OK) return CGTP_ERR_INVALID_ARG;
+  if (n > 0 && (tokens == nullptr || order == nullptr || sorted == nullptr)) return CGTP_ERR_INVALID_ARG;
+  if (n > 0 && (tokens == order || tokens == sorted || order == sorted)) return CGTP_ERR_INVALID_ARG;
+  const cgtp_status st = workspace_ok(workspace, workspace_bytes, need);
+  if (st != CGTP_OK) return st;
+  return launched(launch_token_sort(n, n_rows, tokens, order, sorted, workspace, (cudaStream_t)stream));
+}
+
+cgtp_status cgtp_embed_forward(int n, int n_rows, int width, const int* tokens, const float* table, float scale,
+                               float* out, long long out_stride, void* stream) {
+  if (n < 0 || n > kMaxTokens || n_rows < 0 || width < 0) return CGTP_ERR_INVALID_ARG;
+  if (n > 0 && width > 0 && (tokens == nullptr || (n_rows > 0 && table == nullptr))) return CGTP_ERR_INVALID_ARG;
+  if (!rows_ok(out, n, width, out_stride)) return CGTP_ERR_INVALID_ARG;
+  return launched(launch_embed_fwd(n, n_rows, width, tokens, table, scale, out, out_stride, (cudaStream_t)stream));
+}
+
+cgtp_status cgtp_embed_backward_workspace_size(int n, int width, size_t* bytes) {
+  if (n < 0 || n > kMaxTokens || width < 0 || bytes == nullptr) return CGTP_ERR_INVALID_ARG;
+  *bytes = n == 0 || width == 0 ? 0 : embed_bwd_workspace(n, width);
+  return CGTP_OK;
+}
+
+cgtp_status cgtp_embed_backward(int n, int n_rows, int width, const int* order, const int* sorted,
+                                const float* grad_out, long long grad_stride, float scale, float* grad_table,
+                                void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  if (n_rows < 0 || cgtp_embed_backward_workspace_size(n, width, &need) != CGTP_OK) return CGTP_ERR_INVALID_ARG;
+  if (n_rows == 0 || width == 0) return CGTP_OK;
+  if (grad_table == nullptr || (n > 0 && (order == nullptr || sorted == nullptr))) return CGTP_ERR_INVALID_ARG;
+  if (!rows_ok(grad_out, n, width, grad_stride)) return CGTP_ERR_INVALID_ARG;
+  const cgtp_status st = workspace_ok(workspace, workspace_bytes, need);
+  if (st != CGTP_OK) return st;
+  return launched(launch_embed_bwd(n, n_rows, width, order, sorted, grad_out, grad_stride, scale, grad_table, workspace,
+                                   (cudaStream_t)stream));
+}
+
+cgtp_status cgtp_group_norm_workspace_size(int n, int n_samples, int channels, int groups, size_t* bytes) {
+  if (n < 0 || n > kMaxTokens || n_samples < 0 || channels < 0 || groups < 1 || channels % groups != 0 ||
+      bytes == nullptr)
+    return CGTP_ERR_INVALID_ARG;
+  *bytes = channels == 0 ? 0 : norm_workspace(n, n_samples, channels, groups);
+  return CGTP_OK;
+}
+
+static cgtp_status norm_args(const NormArgs& a, int max_rows, const void* ws, size_t ws_bytes) {
+  size_t need = 0;
+  if (cgtp_group_norm_workspace_size(a.n, a.samples, a.channels, a.groups, &need) != CGTP_OK)
+    return CGTP_ERR_INVALID_ARG;
+  if (max_rows < 0 || (a.act != CGTP_ACT_NONE && a.act != CGTP_ACT_SILU)) return CGTP_ERR_INVALID_ARG;
+  if (a.ptr == nullptr && a.samples != 1) return CGTP_ERR_INVALID_ARG;
+  if (!rows_ok(a.x, a.n, a.channels, a.x_stride)) return CGTP_ERR_INVALID_ARG;
+  if (a.samples > 0 && a.channels > 0 && (a.mean == nullptr || a.rstd == nullptr)) return CGTP_ERR_INVALID_ARG;
+  return workspace_ok(ws, ws_bytes, need);
+}
+
+cgtp_status cgtp_group_norm_forward(int n, int n_samples, int channels, int groups, const int* graph_ptr,
+                                    int max_rows, const float* x, long long x_stride, const float* gamma,
+                                    const float* beta, float eps, cgtp_act act, float* y, long long y_stride,
+                                    float* mean, float* rstd, void* workspace, size_t workspace_bytes,
+                                    void* stream) {
+  NormArgs a{};
+  a.n = n;
+  a.samples = n_samples;
+  a.channels = channels;
+  a.groups = groups;
+  a.ptr = graph_ptr;
+  a.x = x;
+  a.x_stride = x_stride;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.eps = eps;
+  a.act = (int)act;
+  a.y = y;
+  a.y_stride = y_stride;
+  a.mean = mean;
+  a.rstd = rstd;
+  if (!(eps > 0.f)) return CGTP_ERR_INVALID_ARG;
+  const cgtp_status st = norm_args(a, max_rows, workspace, workspace_bytes);
+  if (st != CGTP_OK) return st;
+  if (!rows_ok(y, n, channels, y_stride) || (y == x && y_stride != x_stride)) return CGTP_ERR_INVALID_ARG;
+  return launched(launch_norm_fwd(a, max_rows, workspace, (cudaStream_t)stream));
+}
+
+cgtp_status cgtp_group_norm_backward(int n, int n_samples, int channels, int groups, const int* graph_ptr,
+                                     int max_rows, const float* x, long long x_stride, const float* gamma,
+                                     const float* beta, const float* mean, const float* rstd, cgtp_act act,
+                                     const float* grad_y, long long gy_stride, float* grad_x, long long gx_stride,
+                                     float* grad_gamma, float* grad_beta, void* workspace, size_t workspace_bytes,
+                                     void* stream) {
+  NormArgs a{};
+  a.n = n;
+  a.samples = n_samples;
+  a.channels = channels;
+  a.groups = groups;
+  a.ptr = graph_ptr;
+  a.x = x;
+  a.x_stride = x_stride;
+  a.gamma = gamma;
+  a.beta = beta;
+  a.act = (int)act;
+  a.mean = const_cast<float*>(mean);  // read only in this direction
+  a.rstd = const_cast<float*>(rstd);
+  a.grad_y = grad_y;
+  a.gy_stride = gy_stride;
+  a.grad_x = grad_x;
+  a.gx_stride = gx_stride;
+  a.grad_gamma = grad_gamma;
+  a.grad_beta = grad_beta;
+  const cgtp_status st = norm_args(a, max_rows, workspace, workspace_bytes);
+  if (st != CGTP_OK) return st;
+  if (!rows_ok(grad_y, n, channels, gy_stride)) return CGTP_ERR_INVALID_ARG;
+  if (grad_x != nullptr && (!rows_ok(grad_x, n, channels, gx_stride) || (grad_x == grad_y && gx_stride != gy_stride)))
+    return CGTP_ERR_INVALID_ARG;
+  return launched(launch_norm_bwd(a, max_rows, workspace, (cudaStream_t)stream));
+}
+
+cgtp_status cgtp_orthogonalise_workspace_size(int batch, int rows, int cols, size_t* bytes) {
+  if (batch < 0 || rows < 0 || cols < 0 || batch > 65535 || rows > 65536 || cols > 65536 || bytes == nullptr)
+    return CGTP_ERR_INVALID_ARG;
+  *bytes = batch == 0 || rows == 0 || cols == 0 ? 0 : ortho_workspace(batch, rows, cols);
+  return CGTP_OK;
+}
+
+cgtp_status cgtp_orthogonalise(int batch, int rows, int cols, int steps, float scale, const float* update, float* out,
+                               void* workspace, size_t workspace_bytes, void* stream) {
+  size_t need = 0;
+  if (steps < 1 || steps > 64 || cgtp_orthogonalise_workspace_size(batch, rows, cols, &need) != CGTP_OK)
+    return CGTP_ERR_INVALID_ARG;
+  if (batch == 0 || rows == 0 || cols == 0) return CGTP_OK;
+  if (update == nullptr || out == nullptr) return CGTP_ERR_INVALID_ARG;
+  const cgtp_status st = workspace_ok(workspace, workspace_bytes, need);
+  if (st != CGTP_OK) return st;
+  return launched(launch_ortho(batch, rows, cols, steps, scale, update, out, workspace, (cudaStream_t)stream));
+}
+
+}  // extern "C"

@@ -1,0 +1,500 @@
+// Embedding of tokens (atom species, vocabulary entries) into feature rows,
+// and the table's gradient by sorted tokens, for sm_100a.
+//
+//   out[k][:]        = scale * table[tok[k]][:]        (0 when tok[k] is no row)
+//   grad_table[v][:] = scale * sum_{k: tok[k] = v} grad_out[k][:]
+//
+// Both move data and compute next to nothing: n x width values read and
+// written (forward), read once with n_rows x width written (backward).
+//
+// The gradient sums rows in the order of a stable sort of the tokens, so every
+// sum has one fixed order (no floating-point atomics): the sorted positions
+// are cut into chunks of equal length, one worker (a group of lanes) walks one
+// chunk and writes each run that lies inside it; a run that crosses chunk
+// borders leaves one partial sum per chunk, joined by a second kernel.
+// Equal chunks balance the work whatever the tokens' frequencies are: one row
+// that takes every token and as many rows as tokens cost the same reads.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "train_ops.h"
+
+namespace cgtp {
+namespace {
+
+// ------------------------------------------------------------------ sort
+// Least-significant-digit radix sort of (key, position), 8 bits a pass, where
+// the key of a token outside [0, n_rows) is n_rows (so those come last).
+// Every pass is two steps over tiles of kSortTile tokens: the digit counts
+// of each tile, then the scatter, in which each tile adds up the counts of the
+// tiles before it (and of smaller digits) itself.  The scatter of one pass
+// counts the next pass's digits as it places them (integer atomics: the
+// counts do not depend on their order), so a sort of p passes is p + 1
+// launches.  Beyond kSortScanTiles tiles that sum over tiles, which every tile
+// repeats, would grow with their square: one more launch a pass then turns
+// the counts into prefixes first.  A warp ranks equal digits by ballot of
+// matching lanes in position order, which keeps the sort stable.
+constexpr int kSortThreads = 512;
+constexpr int kSortItems = 8;
+constexpr int kSortTile = kSortThreads * kSortItems;  // tokens per tile
+constexpr int kSortWarps = kSortThreads / 32;
+constexpr int kDigits = 256;
+constexpr int kSortScanTiles = 256;
+
+__device__ __forceinline__ int token_key(int t, int n_rows) { return (unsigned)t < (unsigned)n_rows ? t : n_rows; }
+
+__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(int n, int n_rows, const int* __restrict__ tokens,
+                                                                   int* __restrict__ counts) {
+  __shared__ int c[kDigits];
+  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) c[d] = 0;
+  __syncthreads();
+  const long long base = (long long)blockIdx.x * kSortTile;
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i) {
+    const long long k = base + i * kSortThreads + threadIdx.x;
+    if (k < n) atomicAdd(&c[token_key(tokens[k], n_rows) & (kDigits - 1)], 1);
+  }
+  __syncthreads();
+  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) counts[(long long)blockIdx.x * kDigits + d] = c[d];
+}
+
+// One block per digit: the counts of its digit become the sums over earlier
+// tiles, and their total goes behind the last tile's counts.
+__global__ void __launch_bounds__(kSortThreads) sort_prefix_kernel(int tiles, int* __restrict__ counts) {
+  __shared__ int warp_sums[kSortWarps];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  int carry = 0;
+  for (int b0 = 0; b0 < tiles; b0 += kSortThreads) {
+    int* c = counts + (long long)(b0 + tid) * kDigits + blockIdx.x;
+    const int v = b0 + tid < tiles ? *c : 0;
+    int incl = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) warp_sums[w] = incl;
+    __syncthreads();
+    int base = carry;
+    for (int q = 0; q < kSortWarps; ++q) {
+      if (q < w) base += warp_sums[q];
+      carry += warp_sums[q];
+    }
+    if (b0 + tid < tiles) *c = base + incl - v;
+    __syncthreads();
+  }
+  if (tid == 0) counts[(long long)tiles * kDigits + blockIdx.x] = carry;
+}
+
+// One scatter pass over digit bits [shift, shift + 8).  keys_in = nullptr: the
+// first pass, keys from the tokens and positions 0..n-1.  next_counts
+// (nullable): the next pass's tile counts, zeroed before.
+__global__ void __launch_bounds__(kSortThreads)
+    sort_scatter_kernel(int n, int n_rows, int shift, const int* __restrict__ tokens, const int* __restrict__ keys_in,
+                        const int* __restrict__ pos_in, const int* __restrict__ counts, int* __restrict__ keys_out,
+                        int* __restrict__ pos_out, int* __restrict__ next_counts) {
+  __shared__ int warp_count[kSortWarps][kDigits];
+  __shared__ int start[kDigits];
+  __shared__ int scan[kDigits / 32];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
+  for (int d = tid; d < kSortWarps * kDigits; d += kSortThreads) (&warp_count[0][0])[d] = 0;
+  // start of each digit of this tile: smaller digits of every tile, then the same digit of earlier tiles
+  int before = 0, incl = 0, total = 0;
+  if (tid < kDigits) {
+    if (gridDim.x > kSortScanTiles) {  // prefixes already
+      before = counts[(long long)blockIdx.x * kDigits + tid];
+      total = counts[(long long)gridDim.x * kDigits + tid];
+    } else {
+#pragma unroll 8
+      for (int b = 0; b < (int)gridDim.x; ++b) {
+        const int c = counts[b * kDigits + tid];
+        if (b < (int)blockIdx.x) before += c;
+        total += c;
+      }
+    }
+    incl = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) scan[w] = incl;
+  }
+  __syncthreads();
+  if (tid < kDigits) {
+    int base = 0;
+    for (int q = 0; q < w; ++q) base += scan[q];
+    start[tid] = base + incl - total + before;
+  }
+  // ranks inside the warp's own stretch of kSortItems x 32 consecutive tokens
+  int key[kSortItems], pos[kSortItems], rank[kSortItems];
+  const long long base = (long long)blockIdx.x * kSortTile + w * (32 * kSortItems);
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i) {
+    const long long k = base + 32 * i + lane;
+    key[i] = -1;
+    pos[i] = 0;
+    if (k < n) {
+      key[i] = keys_in == nullptr ? token_key(tokens[k], n_rows) : keys_in[k];
+      pos[i] = pos_in == nullptr ? (int)k : pos_in[k];
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i) {
+    const int d = key[i] < 0 ? kDigits : (key[i] >> shift) & (kDigits - 1);
+    const unsigned same = __match_any_sync(0xffffffffu, d);
+    const int lower = __popc(same & ((1u << lane) - 1u));
+    int seen = 0;
+    if (d < kDigits) seen = warp_count[w][d];
+    __syncwarp();
+    if (d < kDigits && lower == 0) warp_count[w][d] = seen + __popc(same);
+    __syncwarp();
+    rank[i] = seen + lower;
+  }
+  __syncthreads();
+  if (tid < kDigits) {  // the warps' counts become their starts
+    int run = start[tid];
+#pragma unroll
+    for (int q = 0; q < kSortWarps; ++q) {
+      const int c = warp_count[q][tid];
+      warp_count[q][tid] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < kSortItems; ++i) {
+    if (key[i] < 0) continue;
+    const int to = warp_count[w][(key[i] >> shift) & (kDigits - 1)] + rank[i];
+    keys_out[to] = key[i];
+    pos_out[to] = pos[i];
+    if (next_counts != nullptr)
+      atomicAdd(next_counts + (long long)(to / kSortTile) * kDigits + ((key[i] >> (shift + 8)) & (kDigits - 1)), 1);
+  }
+}
+
+int sort_passes(int n_rows) {  // digits of the largest key, n_rows itself
+  int p = 1;
+  while (p < 4 && ((unsigned)n_rows >> (8 * p)) != 0) ++p;
+  return p;
+}
+long long sort_tiles(int n) { return ((long long)n + kSortTile - 1) / kSortTile; }
+
+// --------------------------------------------------------------- gradient
+// A worker is a group of LPR lanes (a power of two) that covers LPR vectors
+// of VEC columns of one row; a warp holds 32 / LPR workers.
+template <int VEC>
+struct Vec {
+  float v[VEC];
+};
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> load_vec(const float* p) {
+  Vec<VEC> r;
+  if constexpr (VEC == 4) {
+    const float4 q = *reinterpret_cast<const float4*>(p);
+    r.v[0] = q.x;
+    r.v[1] = q.y;
+    r.v[2] = q.z;
+    r.v[3] = q.w;
+  } else {
+    r.v[0] = *p;
+  }
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ void store_vec(float* p, const Vec<VEC>& a) {
+  if constexpr (VEC == 4) *reinterpret_cast<float4*>(p) = make_float4(a.v[0], a.v[1], a.v[2], a.v[3]);
+  else *p = a.v[0];
+}
+
+struct EmbedBwdArgs {
+  int n, n_rows, width, chunk, n_chunks, lpr, slices;
+  const int *order, *sorted;
+  const float* grad_out;
+  long long grad_stride;
+  float scale;
+  float* grad_table;
+  float *head, *tail;  // [n_chunks][width] partial sums of runs that cross chunk borders
+};
+
+constexpr int kEmbedThreads = 256;
+constexpr int kEmbedUnroll = 8;
+
+// Blocks below chunk_blocks: one worker per (chunk, column slice).  The other
+// blocks write zeros into the rows that no token has, found by a search of
+// the sorted tokens; they run beside the first ones.
+template <int VEC>
+__global__ void __launch_bounds__(kEmbedThreads) embed_bwd_kernel(EmbedBwdArgs a, int chunk_blocks) {
+  const int lane = threadIdx.x & (a.lpr - 1);
+  if ((int)blockIdx.x >= chunk_blocks) {
+    const long long stride = (long long)(gridDim.x - chunk_blocks) * (kEmbedThreads / 32);
+    const int wl = threadIdx.x & 31;
+    for (long long r0 = ((long long)(blockIdx.x - chunk_blocks) * (kEmbedThreads / 32) + (threadIdx.x >> 5)) * 32;
+         r0 < a.n_rows; r0 += stride * 32) {
+      // each lane searches one of 32 rows, then the warp clears the empty ones together
+      const int r = (int)(r0 + wl);
+      bool empty = false;
+      if (r0 + wl < a.n_rows) {
+        int lo = 0, hi = a.n;  // first position with sorted >= r
+        while (lo < hi) {
+          const int mid = lo + (hi - lo) / 2;
+          if (a.sorted[mid] < r) lo = mid + 1;
+          else hi = mid;
+        }
+        empty = lo >= a.n || a.sorted[lo] != r;
+      }
+      for (unsigned m = __ballot_sync(0xffffffffu, empty); m != 0; m &= m - 1) {
+        float* row = a.grad_table + (r0 + __ffs(m) - 1) * (long long)a.width;
+        Vec<VEC> z{};
+        for (int c = wl * VEC; c < a.width; c += 32 * VEC) store_vec<VEC>(row + c, z);
+      }
+    }
+    return;
+  }
+  const long long worker = ((long long)blockIdx.x * kEmbedThreads + threadIdx.x) / a.lpr;
+  const int chunk = (int)(worker / a.slices), slice = (int)(worker % a.slices);
+  const int col = (slice * a.lpr + lane) * VEC;
+  if (chunk >= a.n_chunks || col >= a.width) return;
+  const int p0 = chunk * a.chunk, p1 = min(a.n - p0, a.chunk) + p0;
+  int run = a.sorted[p0];
+  bool from_before = p0 > 0 && a.sorted[p0 - 1] == run;
+  Vec<VEC> acc{};
+  auto finish = [&](int key) {  // the run ends inside the chunk
+    if (from_before) {
+      store_vec<VEC>(a.head + (long long)chunk * a.width + col, acc);
+    } else if ((unsigned)key < (unsigned)a.n_rows) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) acc.v[j] *= a.scale;
+      store_vec<VEC>(a.grad_table + (long long)key * a.width + col, acc);
+    }
+  };
+  for (int p = p0; p < p1; p += kEmbedUnroll) {
+    int key[kEmbedUnroll];
+    Vec<VEC> g[kEmbedUnroll];
+#pragma unroll
+    for (int i = 0; i < kEmbedUnroll; ++i) {
+      key[i] = -1;
+      g[i] = Vec<VEC>{};
+      if (p + i < p1) {
+        key[i] = a.sorted[p + i];
+        const int k = a.order[p + i];
+        if ((unsigned)k < (unsigned)a.n && (unsigned)key[i] < (unsigned)a.n_rows)
+          g[i] = load_vec<VEC>(a.grad_out + (long long)k * a.grad_stride + col);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kEmbedUnroll; ++i) {
+      if (p + i >= p1) break;
+      if (key[i] != run) {
+        finish(run);
+        run = key[i];
+        from_before = false;
+        acc = Vec<VEC>{};
+      }
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) acc.v[j] += g[i].v[j];
+    }
+  }
+  const bool goes_on = p1 < a.n && a.sorted[p1] == run;
+  if (goes_on && !from_before) store_vec<VEC>(a.tail + (long long)chunk * a.width + col, acc);
+  else finish(run);
+}
+
+// Joins the runs that cross chunk borders: one block per (chunk in which such
+// a run starts, slice); the block's workers take the run's later chunks in
+// turn and their sums meet in shared memory in a fixed order.
+template <int VEC>
+__global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedBwdArgs a) {
+  __shared__ Vec<VEC> part[kEmbedThreads];
+  const int chunk = blockIdx.x, p0 = chunk * a.chunk, p1 = p0 + a.chunk;
+  if (p1 >= a.n) return;
+  const int run = a.sorted[p1 - 1];
+  if (a.sorted[p1] != run || (unsigned)run >= (unsigned)a.n_rows) return;
+  if (p0 > 0 && a.sorted[p0 - 1] == run) return;  // it started earlier
+  int lo = p1, hi = a.n;  // first position behind the run
+  while (lo < hi) {
+    const int mid = lo + (hi - lo) / 2;
+    if (a.sorted[mid] <= run) lo = mid + 1;
+    else hi = mid;
+  }
+  const int last = (lo - 1) / a.chunk;
+  const int lane = threadIdx.x & (a.lpr - 1), worker = threadIdx.x / a.lpr, workers = kEmbedThreads / a.lpr;
+  const int col = (blockIdx.y * a.lpr + lane) * VEC;
+  Vec<VEC> acc{};
+  if (col < a.width) {
+    if (worker == 0) acc = load_vec<VEC>(a.tail + (long long)chunk * a.width + col);
+#pragma unroll 4
+    for (int c = chunk + 1 + worker; c <= last; c += workers) {
+      const Vec<VEC> h = load_vec<VEC>(a.head + (long long)c * a.width + col);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) acc.v[j] += h.v[j];
+    }
+  }
+  part[threadIdx.x] = acc;
+  __syncthreads();
+  for (int o = workers >> 1; o > 0; o >>= 1) {
+    if (worker < o)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) part[threadIdx.x].v[j] += part[threadIdx.x + o * a.lpr].v[j];
+    __syncthreads();
+  }
+  if (worker == 0 && col < a.width) {
+    acc = part[threadIdx.x];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) acc.v[j] *= a.scale;
+    store_vec<VEC>(a.grad_table + (long long)run * a.width + col, acc);
+  }
+}
+
+// ---------------------------------------------------------------- forward
+constexpr int kFwdRows = 4;  // rows per worker: four independent row reads in flight a lane
+
+template <int VEC>
+__global__ void __launch_bounds__(kEmbedThreads)
+    embed_fwd_kernel(int n, int n_rows, int width, int lpr, int slices, const int* __restrict__ tokens,
+                     const float* __restrict__ table, float scale, float* __restrict__ out, long long out_stride) {
+  const int lane = threadIdx.x & (lpr - 1);
+  const long long worker = ((long long)blockIdx.x * kEmbedThreads + threadIdx.x) / lpr;
+  const long long k0 = worker / slices * kFwdRows;
+  const int col = ((int)(worker % slices) * lpr + lane) * VEC;
+  if (col >= width) return;
+  Vec<VEC> v[kFwdRows];
+#pragma unroll
+  for (int i = 0; i < kFwdRows; ++i) {
+    v[i] = Vec<VEC>{};
+    if (k0 + i < n) {
+      const int t = tokens[k0 + i];
+      if ((unsigned)t < (unsigned)n_rows) v[i] = load_vec<VEC>(table + (long long)t * width + col);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < kFwdRows; ++i) {
+    if (k0 + i < n) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[i].v[j] *= scale;
+      store_vec<VEC>(out + (k0 + i) * out_stride + col, v[i]);
+    }
+  }
+}
+
+bool vec4_rows(const void* p, long long stride, int width) {
+  return width % 4 == 0 && stride % 4 == 0 && ((uintptr_t)p & 15u) == 0;
+}
+int lanes_per_row(int width, int vec) {
+  const int need = (width + vec - 1) / vec;
+  int l = 1;
+  while (l < 32 && l < need) l <<= 1;
+  return l;
+}
+// Sorted positions per chunk, a function of the sizes alone (the sums' order
+// does not depend on the device): enough chunks for some 8 000 workers, at
+// least 16 positions so that the partial sums stay a small part of the reads.
+int embed_chunk(int n, int width) {
+  const long long slices = (width + 127) / 128;
+  int c = 16;
+  while (c < 256 && (long long)n * slices / c > 8192) c <<= 1;
+  return c;
+}
+
+}  // namespace
+
+size_t token_sort_workspace(int n, int n_rows) {
+  const int p = sort_passes(n_rows);
+  const size_t counts = sizeof(int) * (size_t)(sort_tiles(n) + 1) * kDigits;
+  return (size_t)(p > 1 ? 2 : 1) * counts + (p > 1 ? 2 * pad256(sizeof(int) * (size_t)n) : 0);
+}
+
+cudaError_t launch_token_sort(int n, int n_rows, const int* tokens, int* order, int* sorted, void* ws, cudaStream_t stream) {
+  if (n == 0) return cudaSuccess;
+  const int passes = sort_passes(n_rows);
+  const unsigned tiles = (unsigned)sort_tiles(n);
+  const size_t counts_bytes = sizeof(int) * ((size_t)tiles + 1) * kDigits, n_bytes = pad256(sizeof(int) * (size_t)n);
+  char* at = (char*)ws;
+  int* counts[2] = {(int*)at, (int*)(at + counts_bytes)};
+  int* tmp_keys = (int*)(at + 2 * counts_bytes);
+  int* tmp_pos = (int*)(at + 2 * counts_bytes + n_bytes);
+  sort_count_kernel<<<tiles, kSortThreads, 0, stream>>>(n, n_rows, tokens, counts[0]);
+  cudaError_t e = cudaGetLastError();
+  const int *keys = nullptr, *pos = nullptr;
+  for (int p = 0; p < passes && e == cudaSuccess; ++p) {
+    // the last pass writes the results; the passes before it alternate with the temporaries
+    const bool to_out = (passes - 1 - p) % 2 == 0;
+    int* ko = to_out ? sorted : tmp_keys;
+    int* po = to_out ? order : tmp_pos;
+    int* next = p + 1 < passes ? counts[(p + 1) & 1] : nullptr;
+    if (next != nullptr) e = cudaMemsetAsync(next, 0, sizeof(int) * (size_t)tiles * kDigits, stream);
+    if (e == cudaSuccess && tiles > kSortScanTiles) {
+      sort_prefix_kernel<<<kDigits, kSortThreads, 0, stream>>>((int)tiles, counts[p & 1]);
+      e = cudaGetLastError();
+    }
+    if (e != cudaSuccess) break;
+    sort_scatter_kernel<<<tiles, kSortThreads, 0, stream>>>(n, n_rows, 8 * p, tokens, keys, pos, counts[p & 1], ko, po,
+                                                            next);
+    e = cudaGetLastError();
+    keys = ko;
+    pos = po;
+  }
+  return e;
+}
+
+cudaError_t launch_embed_fwd(int n, int n_rows, int width, const int* tokens, const float* table, float scale,
+                             float* out, long long out_stride, cudaStream_t stream) {
+  if (n == 0 || width == 0) return cudaSuccess;
+  const bool v4 = vec4_rows(table, width, width) && vec4_rows(out, out_stride, width);
+  const int vec = v4 ? 4 : 1, lpr = lanes_per_row(width, vec), slices = (width + lpr * vec - 1) / (lpr * vec);
+  const long long threads = ((long long)n + kFwdRows - 1) / kFwdRows * slices * lpr;
+  const long long blocks = (threads + kEmbedThreads - 1) / kEmbedThreads;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  if (v4)
+    embed_fwd_kernel<4><<<(unsigned)blocks, kEmbedThreads, 0, stream>>>(n, n_rows, width, lpr, slices, tokens, table,
+                                                                        scale, out, out_stride);
+  else
+    embed_fwd_kernel<1><<<(unsigned)blocks, kEmbedThreads, 0, stream>>>(n, n_rows, width, lpr, slices, tokens, table,
+                                                                        scale, out, out_stride);
+  return cudaGetLastError();
+}
+
+size_t embed_bwd_workspace(int n, int width) {
+  const size_t chunks = ((size_t)n + embed_chunk(n, width) - 1) / embed_chunk(n, width);
+  return 2 * pad256(sizeof(float) * chunks * (size_t)width);
+}
+
+template <int VEC>
+static cudaError_t embed_bwd(EmbedBwdArgs a, cudaStream_t stream) {
+  a.lpr = lanes_per_row(a.width, VEC);
+  a.slices = (a.width + a.lpr * VEC - 1) / (a.lpr * VEC);
+  const long long blocks = ((long long)a.n_chunks * a.slices * a.lpr + kEmbedThreads - 1) / kEmbedThreads;
+  long long clear = ((long long)a.n_rows + kEmbedThreads - 1) / kEmbedThreads;
+  if (clear > 1024) clear = 1024;
+  if (blocks + clear > 0x7fffffffLL || a.slices > 65535) return cudaErrorInvalidValue;
+  embed_bwd_kernel<VEC><<<(unsigned)(blocks + clear), kEmbedThreads, 0, stream>>>(a, (int)blocks);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess || a.n_chunks < 2) return e;
+  embed_join_kernel<VEC><<<dim3((unsigned)(a.n_chunks - 1), (unsigned)a.slices), kEmbedThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_embed_bwd(int n, int n_rows, int width, const int* order, const int* sorted, const float* grad_out,
+                             long long grad_stride, float scale, float* grad_table, void* ws, cudaStream_t stream) {
+  if (n_rows == 0 || width == 0) return cudaSuccess;
+  if (n == 0) return cudaMemsetAsync(grad_table, 0, sizeof(float) * (size_t)n_rows * width, stream);
+  EmbedBwdArgs a{};
+  a.n = n;
+  a.n_rows = n_rows;
+  a.width = width;
+  a.chunk = embed_chunk(n, width);
+  a.n_chunks = (int)(((long long)n + a.chunk - 1) / a.chunk);
+  a.order = order;
+  a.sorted = sorted;
+  a.grad_out = grad_out;
+  a.grad_stride = grad_stride;
+  a.scale = scale;
+  a.grad_table = grad_table;
+  a.head = (float*)ws;
+  a.tail = (float*)((char*)ws + pad256(sizeof(float) * (size_t)a.n_chunks * width));
+  if (vec4_rows(grad_out, grad_stride, width) && vec4_rows(grad_table, width, width)) return embed_bwd<4>(a, stream);
+  return embed_bwd<1>(a, stream);
+}
+
+}  // namespace cgtp

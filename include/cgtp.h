@@ -465,6 +465,109 @@ cgtp_status cgtp_cp_backward(cgtp_plan plan, int rank, int batch, const float* A
                              float* grad_x, float* grad_y, float* grad_A, float* grad_B, float* grad_C,
                              void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Token embedding (additions of this library): the learned rows of atom
+ * species, or of any other vocabulary, as node features, and the table's
+ * gradient by sorted tokens.  cgtp_gather_rows / cgtp_scatter_add_rows move
+ * rows for indices without repeats; here a token may come any number of times.
+ *   out[k][:]        = scale * table[tokens[k]][:]
+ *   grad_table[v][:] = scale * sum_{k: tokens[k] = v} grad_out[k][:]
+ * tokens: device [n], any values; one outside [0, n_rows) stands for no token
+ * (padding): its output row is zero and it has no part in the gradient.
+ * table, grad_table: [n_rows][width] contiguous.  Rows of out and grad_out
+ * start out_stride and grad_stride floats apart (>= width), so the l = 0 block
+ * of features [n][(lmax+1)^2][width] is written and read in place (stride
+ * (lmax+1)^2 * width; the other blocks are not touched).  Any width; float4
+ * accesses when width and the strides are multiples of 4 and the pointers
+ * 16-byte aligned.  n <= 2^30.
+ *
+ * cgtp_token_sort: a stable sort of the tokens, made once for a batch and used
+ * by every gradient of it: sorted[k] ascending (n_rows for tokens outside
+ * [0, n_rows), which come last), order[k] the position that sorted[k] came
+ * from; equal tokens keep their order.  workspace: device, 256-byte aligned,
+ * of the size cgtp_token_sort_workspace_size reports.
+ * cgtp_embed_backward: order and sorted as cgtp_token_sort wrote them for the
+ * same n_rows.  Every row of grad_table is overwritten (zero for a row without
+ * tokens).  The sums run in the order of the sort, cut into chunks by n and
+ * width alone: equal inputs give equal bits.  Entries of order and sorted that
+ * are out of range are left out, never followed.
+ * ------------------------------------------------------------------------- */
+cgtp_status cgtp_token_sort_workspace_size(int n, int n_rows, size_t* bytes);
+cgtp_status cgtp_token_sort(int n, int n_rows, const int* tokens, int* order, int* sorted,
+                            void* workspace, size_t workspace_bytes, void* stream);
+cgtp_status cgtp_embed_forward(int n, int n_rows, int width, const int* tokens, const float* table,
+                               float scale, float* out, long long out_stride, void* stream);
+cgtp_status cgtp_embed_backward_workspace_size(int n, int width, size_t* bytes);
+cgtp_status cgtp_embed_backward(int n, int n_rows, int width, const int* order, const int* sorted,
+                                const float* grad_out, long long grad_stride, float scale,
+                                float* grad_table, void* workspace, size_t workspace_bytes,
+                                void* stream);
+
+/* Activation of the group norm. */
+typedef enum { CGTP_ACT_NONE = 0, CGTP_ACT_SILU = 1 } cgtp_act;
+
+/* ---------------------------------------------------------------------------
+ * Group norm with an activation over scalar node features, channels last,
+ * normalised per graph (an addition of this library; the activation is the
+ * radial network's SiLU).  A sample is the rows of one graph, graph_ptr[s] to
+ * graph_ptr[s+1] (device [n_samples+1], as for cgtp_graph_build), or all n
+ * rows when graph_ptr is NULL (n_samples 1).  Over the rows of a sample and
+ * the channels of one of `groups` equal groups:
+ *   h = (x - mean) * rstd,  rstd = 1 / sqrt(var + eps)  (var biased)
+ *   y = act(gamma * h + beta)
+ * x, y, grad_y, grad_x: rows of `channels` floats, x_stride, ... floats apart
+ * (>= channels), so the l = 0 block of [n][(lmax+1)^2][mult] is used in place
+ * and an equivariant feature stays one.  gamma, beta: [channels], nullable (1
+ * and 0).  mean, rstd: [n_samples][groups], written by the forward (0 and
+ * 1/sqrt(eps) for a graph without rows) and read by the backward.  y may be x;
+ * grad_x may be grad_y.  Rows outside every sample (before graph_ptr[0], behind
+ * graph_ptr[n_samples]) have no part in any result and are left as they were.  Statistics
+ * and sums in fp32 over deviations from the mean; fixed order (no atomics).
+ * channels must be a multiple of groups (CGTP_ERR_INVALID_ARG otherwise).
+ * max_rows: a bound on the rows of a sample where the caller knows one, 0
+ * otherwise; it chooses how the work is split, never the result's validity.
+ * workspace: device, 256-byte aligned, of the size
+ * cgtp_group_norm_workspace_size reports (for either direction).
+ *
+ * Backward: grad_x (nullable), grad_gamma and grad_beta ([channels], nullable),
+ * all overwritten; x, gamma, beta, mean, rstd as in the forward.
+ * ------------------------------------------------------------------------- */
+cgtp_status cgtp_group_norm_workspace_size(int n, int n_samples, int channels, int groups,
+                                           size_t* bytes);
+cgtp_status cgtp_group_norm_forward(int n, int n_samples, int channels, int groups,
+                                    const int* graph_ptr, int max_rows, const float* x,
+                                    long long x_stride, const float* gamma, const float* beta,
+                                    float eps, cgtp_act act, float* y, long long y_stride,
+                                    float* mean, float* rstd, void* workspace,
+                                    size_t workspace_bytes, void* stream);
+cgtp_status cgtp_group_norm_backward(int n, int n_samples, int channels, int groups,
+                                     const int* graph_ptr, int max_rows, const float* x,
+                                     long long x_stride, const float* gamma, const float* beta,
+                                     const float* mean, const float* rstd, cgtp_act act,
+                                     const float* grad_y, long long gy_stride, float* grad_x,
+                                     long long gx_stride, float* grad_gamma, float* grad_beta,
+                                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Orthogonalised updates (an addition of this library): each matrix of a stack
+ * update [batch][rows][cols] (batch <= 65535, rows and cols <= 65536), such as the gradient of the mixing matrices
+ * [n_paths][mult][mult_out] that cgtp_uvw_backward returns, is brought near
+ * the closest matrix with orthonormal rows or columns by Newton-Schulz
+ * products, as the Muon optimiser does:
+ *   X = G / (|G|_F + 1e-7)
+ *   steps times: A = X X^T, X <- a X + (b A + c A A) X,  (a, b, c) = (3.4445, -4.7750, 2.0315)
+ *   out = scale * X
+ * (on the transposed matrix where rows > cols).  1 <= steps <= 64; out may be
+ * update.  A matrix of zeros gives zeros; one with a NaN or an infinity gives
+ * NaN and leaves the others alone.  The products are fp32-accurate.
+ * workspace: device, 256-byte aligned, of the size
+ * cgtp_orthogonalise_workspace_size reports.
+ * ------------------------------------------------------------------------- */
+cgtp_status cgtp_orthogonalise_workspace_size(int batch, int rows, int cols, size_t* bytes);
+cgtp_status cgtp_orthogonalise(int batch, int rows, int cols, int steps, float scale,
+                               const float* update, float* out, void* workspace,
+                               size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
