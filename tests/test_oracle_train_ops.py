@@ -115,5 +115,5 @@ def test_host_errors():
     assert ns(1, 4, 4, 0, f(1), P, P, P, big, None) == 1
     assert ns(1, 4, 4, 65, f(1), P, P, P, big, None) == 1
     assert ns(1, 4, 4, 5, f(1), None, P, P, big, None) == 1
-    assert ns(1, 4, 4, 5, f(1), P, P, None, 0, None) == 7
+    assert ns(1, 400, 400, 5, f(1), P, P, None, 0, None) == 7
     assert ns(0, 4, 4, 5, f(1), None, None, None, 0, None) == 0                   # nothing to do
