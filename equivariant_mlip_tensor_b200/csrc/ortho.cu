@@ -100,19 +100,27 @@ __global__ void __launch_bounds__(256)
 // ---------------------------------------------------------- the short side up to 128
 // All steps of one matrix in one launch: a cluster of 1, 2, 4 or 8 blocks holds
 // X, each its own columns, as fp16 pairs in shared memory from the first step
-// to the last; A and a + b A + c A A (at most 128 x 128) are in every block.
+// to the last; A and then b A + c A A (at most 128 x 128) are in every block.
 // The same tile of X is read along its rows for X X^T and down its rows for
 // the last product.  With more than one block, the blocks' parts of X X^T meet
 // in cluster shared memory: each block sums its share of the entries over the
-// blocks in order and writes it to all.
-constexpr int kSmallThreads = 256;
-constexpr int kSmallSide = 128;                // rows of X
-constexpr int kSmallColumns = 256;             // columns of X in one block
+// blocks in a fixed order and writes it to all.
+//
+// The diagonals of A and of P = b A + c A A stay out of the operands and are
+// applied in fp32: with A = D + R, A A = D D + D R + R D + R R, and P X likewise.
+// A tensor-core accumulator rounds towards zero at every addition, so a large
+// diagonal term would come out too small by the same 2e-7 everywhere, and
+// a X + P X loses most of its leading digits when the values are near 1
+// (64 x 1920: 3.4e-6 of the result with the diagonals inside, FIXME without).
+constexpr int kSmallThreads = 512;  // and one more warp, which issues the products
+constexpr int kSmallSide = 128;     // rows of X
+constexpr int kSmallColumns = 256;  // columns of X in one block
 constexpr float kXScale = 16384.f, kPScale = 8192.f;
 
 struct SmallArgs {
-  int rows, cols, steps, m, n, tall;
+  int rows, cols, steps, m, n, tall, vec4;
   int mp, nj;  // rows (padded to 16) and columns of X per block (a multiple of 16)
+  int parts;   // accumulators of X X^T
   float scale;
   const float* g;
   float* out;
@@ -133,74 +141,122 @@ __host__ __device__ inline SmallLayout small_layout(int mp, int nj, int blocks) 
   L.part_stride = mp + 4;  // floats: rows 16 bytes apart modulo 128, no bank conflicts of 16-byte stores
   const int part = blocks > 1 ? mp * L.part_stride * 4 : 0;
   const int a_bytes = 2 * L.a_set > part ? 2 * L.a_set : part;
-  L.bytes = 2 * L.x_set + a_bytes + (128 - mp) * 128 + 1024;
+  L.bytes = 2 * L.x_set + a_bytes + (kSmallSide - mp) * 128 + 1024;
   return L;
 }
 
-// Element (r, c) of X before scaling: row r of G, or column r where G is tall.
-__device__ __forceinline__ float small_input(const SmallArgs& a, const float* g, int r, int c) {
-  if (r >= a.m || c >= a.n) return 0.f;
-  return g[a.tall ? (long long)c * a.cols + r : (long long)r * a.cols + c];
+// Eight elements of X before scaling from column c on: of row r of G, or of its column r where G is tall.
+__device__ __forceinline__ void small_input(const SmallArgs& a, const float* g, int r, int c, float (&v)[8]) {
+  if (a.vec4 && r < a.m && c + 8 <= a.n) {
+    const float4* p = reinterpret_cast<const float4*>(g + (long long)r * a.cols + c);
+    const float4 x = p[0], y = p[1];
+    v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+    v[4] = y.x, v[5] = y.y, v[6] = y.z, v[7] = y.w;
+    return;
+  }
+  const float* p = a.tall ? g + (long long)c * a.cols + r : g + (long long)r * a.cols + c;
+  const long long next = a.tall ? a.cols : 1;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = r < a.m && c + i < a.n ? p[i * next] : 0.f;
 }
 
-__global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(SmallArgs a, int blocks) {
+// The products of one contraction in the order low high, high low, high high:
+// small terms before large ones.  da, db: descriptors of the high parts;
+// la, lb: offsets of the low ones; sb: advance of b per step of 16; jump: the
+// extra advance from a tile's end to the next (all in 16-byte units).  Run by a
+// whole warp, issued by one lane.
+__device__ __forceinline__ void issue_products(uint32_t tmem, uint64_t da, uint64_t db, uint32_t la, uint32_t lb,
+                                               uint32_t jump, uint32_t sb, uint32_t jb, int first, int last,
+                                               uint32_t idesc, uint32_t issue) {
+#pragma unroll 1
+  for (int i = first; i < last; ++i) {
+    const uint64_t x = da + 2 * i + (i >> 2) * jump, y = db + sb * i + (i >> 2) * jb;
+    tc::mma(tmem, x + la, y, idesc, i > first, issue);
+    tc::mma(tmem, x, y + lb, idesc, true, issue);
+  }
+#pragma unroll 1
+  for (int i = first; i < last; ++i)
+    tc::mma(tmem, da + 2 * i + (i >> 2) * jump, db + sb * i + (i >> 2) * jb, idesc, true, issue);
+}
+
+__global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(SmallArgs a, int blocks) {
   extern __shared__ uint8_t raw[];
   __shared__ double sums[kSmallThreads / 32];
   __shared__ double block_sum;
+  __shared__ __align__(16) float a_diag[kSmallSide];  // diagonal of A
+  __shared__ float p_diag[kSmallSide];  // diagonal of P
   __shared__ uint32_t tmem_slot;
-  __shared__ uint64_t bar_word;
+  __shared__ uint64_t bars[2];
   const SmallLayout L = small_layout(a.mp, a.nj, blocks);
   uint8_t* base = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
   uint8_t* xs = base;
   uint8_t* as = base + 2 * L.x_set;
   float* part = reinterpret_cast<float*>(as);
-  const uint32_t x_addr = tc::smem_addr(xs), a_addr = tc::smem_addr(as), bar = tc::smem_addr(&bar_word);
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t x_addr = tc::smem_addr(xs), a_addr = tc::smem_addr(as);
+  const uint32_t done = tc::smem_addr(&bars[0]), ready = tc::smem_addr(&bars[1]);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const bool issuer = warp == kSmallThreads / 32;
   const int rank = blockIdx.x % blocks, matrix = blockIdx.x / blocks;
   const int c0 = rank * a.nj;
   const float* g = a.g + (long long)matrix * a.rows * a.cols;
   float* out = a.out + (long long)matrix * a.rows * a.cols;
   uint32_t columns = 32;
-  while ((int)columns < a.mp || (int)columns < a.nj) columns <<= 1;
+  while ((int)columns < a.mp * a.parts || (int)columns < a.nj) columns <<= 1;
 
-  if (warp == 0) tc::tmem_alloc(tc::smem_addr(&tmem_slot), columns);
-  if (tid == 0) tc::mbar_init(bar, 1);
-
-  // Frobenius norm, squares in 64 bits: they neither overflow nor vanish
-  const int units = a.nj / 8;  // 8-column units of a row
-  double s = 0.0;
-  for (int q = tid; q < a.mp * units; q += kSmallThreads) {
-    const int r = a.tall ? q % a.mp : q / units, u = a.tall ? q / a.mp : q % units;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const double v = small_input(a, g, r, c0 + 8 * u + i);
-      s = fma(v, v, s);
+  if (issuer) {
+    tc::tmem_alloc(tc::smem_addr(&tmem_slot), columns);
+    if (lane == 0) {
+      tc::mbar_init(done, 1);
+      tc::mbar_init(ready, kSmallThreads / 32);
     }
+  }
+  // X once from memory; the Frobenius norm from squares in 64 bits, which
+  // neither overflow nor vanish
+  constexpr int kMost = kSmallSide * kSmallColumns / 8 / kSmallThreads;  // 8-column units a thread
+  const int units = a.nj / 8, all_units = issuer ? 0 : a.mp * units;
+  float v[kMost][8];
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    if (k * kSmallThreads >= all_units) break;
+    const int q = tid + k * kSmallThreads;
+    const int r = a.tall ? q % a.mp : q / units, u = a.tall ? q / a.mp : q % units;
+    small_input(a, g, q < all_units ? r : a.m, c0 + 8 * u, v[k]);
+  }
+  double s = 0.0;
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    if (k * kSmallThreads >= all_units) break;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = fma((double)v[k][i], (double)v[k][i], s);
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if (lane == 0) sums[warp] = s;
+  if (lane == 0 && !issuer) sums[warp] = s;
   __syncthreads();
-  if (tid == 0) {
-    s = 0.0;
-    for (int w = 0; w < kSmallThreads / 32; ++w) s += sums[w];
-    block_sum = s;
-  }
-  if (blocks > 1) tc::cluster_sync();
-  else __syncthreads();
   s = 0.0;
-  for (int k = 0; k < blocks; ++k)
-    s += blocks > 1 ? tc::peer_load_double(tc::peer_addr(tc::smem_addr(&block_sum), k)) : block_sum;
-  const double inv = 1.0 / (sqrt(s) + kNsEps);
-
-  // X as fp16 pairs; rows m.. and columns n.. are zero
-  for (int q = tid; q < a.mp * units; q += kSmallThreads) {
-    const int r = a.tall ? q % a.mp : q / units, u = a.tall ? q / a.mp : q % units;
-    float v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)(small_input(a, g, r, c0 + 8 * u + i) * inv);
+  for (int w = 0; w < kSmallThreads / 32; ++w) s += sums[w];
+  if (blocks > 1) {
+    if (tid == 0) block_sum = s;
+    tc::cluster_sync();
+    s = 0.0;
+    for (int k = 0; k < blocks; ++k) s += tc::peer_load_double(tc::peer_addr(tc::smem_addr(&block_sum), k));
+  }
+  // 2^14 / norm as f 2^(e1 + e2), each factor a normal fp32 number
+  int e;
+  const float f = (float)frexp(kXScale / (sqrt(s) + kNsEps), &e);
+  const float s1 = ldexpf(1.f, e / 2), s2 = ldexpf(f, e - e / 2);
+#pragma unroll
+  for (int k = 0; k < kMost; ++k) {
+    if (k * kSmallThreads >= all_units) break;
+    const int q = tid + k * kSmallThreads;
+    if (q >= all_units) continue;
+    const int r = a.tall ? q % a.mp : q / units, u = a.tall ? q / a.mp : q % units;
+    float2 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = make_float2(v[k][2 * i] * s1 * s2, v[k][2 * i + 1] * s1 * s2);
     uint4 hi, lo;
-    tc::split8(v, kXScale, hi, lo);
+    tc::split8(w, hi, lo);
     const uint32_t at = (u >> 3) * a.mp * 128 + tc::tile_unit(r, u & 7);
     *reinterpret_cast<uint4*>(xs + at) = hi;
     *reinterpret_cast<uint4*>(xs + L.x_set + at) = lo;
@@ -209,188 +265,237 @@ __global__ void __launch_bounds__(kSmallThreads, 1) ortho_small_kernel(SmallArgs
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = tmem_slot;
-
-  // One thread issues the three products of a contraction: low high, high low, high high
-  const uint32_t row_set = a.mp * 128;
-  auto rows_by_rows = [&](uint32_t addr, uint32_t set, int k) {  // tile tile^T
-    for (int p = 0; p < 3; ++p) {
-      const uint32_t oa = p == 0 ? set : 0, ob = p == 1 ? set : 0;
-      for (int i = 0; i < k / 16; ++i) {
-        const uint32_t at = addr + (i >> 2) * row_set + (i & 3) * 32;
-        tc::mma(tmem, tc::desc_k(at + oa), tc::desc_k(at + ob), tc::instruction(a.mp, false), p > 0 || i > 0);
-      }
-    }
-    tc::commit(bar);
-  };
-  auto rows_by_columns = [&]() {  // P X
-    for (int p = 0; p < 3; ++p) {
-      const uint32_t oa = p == 0 ? L.a_set : 0, ob = p == 1 ? L.x_set : 0;
-      for (int i = 0; i < a.mp / 16; ++i)
-        tc::mma(tmem, tc::desc_k(a_addr + oa + (i >> 2) * row_set + (i & 3) * 32),
-                tc::desc_mn(x_addr + ob + i * 2048, row_set), tc::instruction(a.nj, true), p > 0 || i > 0);
-    }
-    tc::commit(bar);
-  };
-  // this thread's row of the accumulator, and every other 16 of its columns
-  const int r = (warp & 3) * 32 + lane, half = warp >> 2;
-  const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
-  const bool live = (warp & 3) * 32 < a.mp;  // the warp's rows hold part of the result
-  uint32_t parity = 0;
+  const uint32_t tmem = tmem_slot, row_set = a.mp * 128;
+  uint32_t done_parity = 0, ready_parity = 0;
   bool ok = true;
-  auto wait = [&]() {
-    if (ok) ok = tc::mbar_wait(bar, parity);
-    parity ^= 1;
-    tc::fence_after_sync();
-  };
-  auto ready = [&]() {  // what the threads wrote is there for the next products
-    tc::fence_async();
-    tc::fence_before_sync();
-    __syncthreads();
-    tc::fence_after_sync();
-  };
 
-  for (int step = 0; step < a.steps; ++step) {
-    // A = X X^T
-    if (tid == 0) rows_by_rows(x_addr, L.x_set, a.nj);
-    wait();
-    if (live) {
-      for (int c = half * 16; c < a.mp; c += 32) {
-        float v[16];
-        tc::tmem_load16(t_row + c, v);
-        if (r < a.mp) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] *= 1.f / (kXScale * kXScale);
-          if (blocks > 1) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              reinterpret_cast<float4*>(part + r * L.part_stride + c)[i] =
-                  make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-          } else {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float w[8] = {v[8 * h],     v[8 * h + 1], v[8 * h + 2], v[8 * h + 3],
-                                  v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]};
-              uint4 hi, lo;
-              tc::split8(w, kXScale, hi, lo);
-              const uint32_t at = (c >> 6) * row_set + tc::tile_unit(r, ((c >> 3) + h) & 7);
-              *reinterpret_cast<uint4*>(as + at) = hi;
-              *reinterpret_cast<uint4*>(as + L.a_set + at) = lo;
-            }
-          }
-        }
+  if (issuer) {
+    const uint32_t issue = tc::elect(), jump = row_set / 16 - 8;
+    const uint64_t x_k = tc::desc_k(x_addr), a_k = tc::desc_k(a_addr), x_mn = tc::desc_mn(x_addr, row_set);
+    const uint32_t square = tc::instruction(a.mp, false), wide = tc::instruction(a.nj, true);
+    const uint32_t xl = L.x_set / 16, al = L.a_set / 16;
+    auto wait_ready = [&]() {
+      if (ok) ok = tc::mbar_wait(ready, ready_parity);
+      ready_parity ^= 1;
+      tc::fence_after_sync();
+    };
+    for (int step = 0; step < a.steps; ++step) {
+      if (step > 0) wait_ready();
+      for (int p = 0; p < a.parts; ++p)
+        issue_products(tmem + p * a.mp, x_k, x_k, xl, xl, jump, 2, jump, p * (a.nj / 16) / a.parts,
+                       (p + 1) * (a.nj / 16) / a.parts, square, issue);
+      tc::commit(done, issue);
+      if (blocks > 1) {
+        __syncwarp();
+        for (int k = 0; k < 3; ++k) tc::cluster_sync();
       }
+      wait_ready();
+      issue_products(tmem, a_k, a_k, al, al, jump, 2, jump, 0, a.mp / 16, square, issue);
+      tc::commit(done, issue);
+      wait_ready();
+      issue_products(tmem, a_k, x_mn, al, xl, jump, 128, 0, 0, a.mp / 16, wide, issue);
+      tc::commit(done, issue);
+      __syncwarp();
     }
-    if (blocks > 1) {
-      tc::cluster_sync();  // every block's part is there
-      const int row_units = a.mp / 8, all = a.mp * row_units;
-      const int u0 = rank * all / blocks, u1 = (rank + 1) * all / blocks;
-      constexpr int kMost = kSmallSide * kSmallSide / 8 / 2 / kSmallThreads;  // units a thread, 2 blocks
-      uint4 hi[kMost], lo[kMost];
-#pragma unroll
-      for (int k = 0; k < kMost; ++k) {
-        const int u = u0 + tid + k * kSmallThreads;
-        float w[8] = {};
-        if (u < u1) {
-          const uint32_t at = a_addr + ((u / row_units) * L.part_stride + u % row_units * 8) * 4;
-          for (int b = 0; b < blocks; ++b) {
-            const uint32_t from = tc::peer_addr(at, b);
-            const float4 p = tc::peer_load4(from), q = tc::peer_load4(from + 16);
-            w[0] += p.x, w[1] += p.y, w[2] += p.z, w[3] += p.w;
-            w[4] += q.x, w[5] += q.y, w[6] += q.z, w[7] += q.w;
-          }
-        }
-        tc::split8(w, kXScale, hi[k], lo[k]);
-      }
-      tc::cluster_sync();  // every part has been read: A may take its place
-#pragma unroll
-      for (int k = 0; k < kMost; ++k) {
-        const int u = u0 + tid + k * kSmallThreads;
-        if (u >= u1) continue;
-        const int rr = u / row_units, cu = u % row_units;
-        const uint32_t at = a_addr + (cu >> 3) * row_set + tc::tile_unit(rr, cu & 7);
-        for (int b = 0; b < blocks; ++b) {
-          tc::peer_store16(tc::peer_addr(at, b), hi[k]);
-          tc::peer_store16(tc::peer_addr(at + L.a_set, b), lo[k]);
-        }
-      }
+  } else {
+    // this thread's row of the accumulator and its columns, 16 of every 64
+    const int r = (warp & 3) * 32 + lane, first = (warp >> 2) * 16;
+    const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const bool live = (warp & 3) * 32 < a.mp;  // the warp's rows hold part of the result
+    const bool row_on = r < a.mp;
+    auto wait_done = [&]() {
+      if (ok) ok = tc::mbar_wait(done, done_parity);
+      done_parity ^= 1;
+      tc::fence_after_sync();
+    };
+    auto wrote = [&]() {  // what the warp wrote is there for the next products
       tc::fence_async();
-      tc::cluster_sync();
-    }
-    ready();
-    // A A
-    if (tid == 0) rows_by_rows(a_addr, L.a_set, a.mp);
-    wait();
-    if (live) {
-      for (int c = half * 16; c < a.mp; c += 32) {
-        float v[16];
-        tc::tmem_load16(t_row + c, v);
-        if (r < a.mp) {
+      tc::fence_before_sync();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(ready);
+    };
+    auto all_wrote = [&]() {  // and what the other warps wrote, for this one
+      if (ok) ok = tc::mbar_wait(ready, ready_parity);
+      ready_parity ^= 1;
+    };
+    // f(column, 8 values) for the thread's columns below `end`; `parts` accumulators are added
+    auto for_columns = [&](int end, int parts, auto&& f) {
+      if (!live) return;
+      for (int c = first; c < end; c += 64) {
+        uint32_t p[16];
+        tc::tmem_load16(t_row + c, p);
+        tc::tmem_wait(p);
+        float2 w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = make_float2(__uint_as_float(p[2 * i]), __uint_as_float(p[2 * i + 1]));
+        for (int k = 1; k < parts; ++k) {
+          tc::tmem_load16(t_row + k * a.mp + c, p);
+          tc::tmem_wait(p);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            w[i] = __fadd2_rn(w[i], make_float2(__uint_as_float(p[2 * i]), __uint_as_float(p[2 * i + 1])));
+        }
+        if (row_on) {
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t at = (c >> 6) * row_set + tc::tile_unit(r, ((c >> 3) + h) & 7);
-            uint4 hi = *reinterpret_cast<const uint4*>(as + at), lo = *reinterpret_cast<const uint4*>(as + L.a_set + at);
-            float w[8];
-            tc::join8(hi, lo, 1.f / kXScale, w);
+            float2 u[4] = {w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
+            f(c + 8 * h, u);
+          }
+        }
+        __syncwarp();
+      }
+    };
+    // the element of column `col` out of eight, which becomes 0
+    auto take = [](float2(&w)[4], int col) {
+      float d = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (col == 2 * i) d = w[i].x, w[i].x = 0.f;
+        if (col == 2 * i + 1) d = w[i].y, w[i].y = 0.f;
+      }
+      return d;
+    };
+    auto place = [&](int c) { return (c >> 6) * row_set + tc::tile_unit(r, (c >> 3) & 7); };
+    auto put = [&](uint8_t* tiles, int set, uint32_t at, const float2(&w)[4]) {
+      uint4 hi, lo;
+      tc::split8(w, hi, lo);
+      *reinterpret_cast<uint4*>(tiles + at) = hi;
+      *reinterpret_cast<uint4*>(tiles + set + at) = lo;
+    };
+    auto get = [&](const uint8_t* tiles, int set, uint32_t at, float2(&w)[4]) {
+      tc::join8(*reinterpret_cast<const uint4*>(tiles + at), *reinterpret_cast<const uint4*>(tiles + set + at), w);
+    };
+    auto pair = [](float v) { return make_float2(v, v); };
+
+    for (int step = 0; step < a.steps; ++step) {
+      // A = X X^T: the diagonal to a_diag, the rest (x 2^14) to the tiles
+      wait_done();
+      for_columns(a.mp, a.parts, [&](int c, float2(&w)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __fmul2_rn(w[i], pair(1.f / kXScale));
+        if (blocks > 1) {
+          float4* to = reinterpret_cast<float4*>(part + r * L.part_stride + c);
+          to[0] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
+          to[1] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
+        } else {
+          if ((r >> 3) == (c >> 3)) a_diag[r] = take(w, r & 7) * (1.f / kXScale);
+          put(as, L.a_set, place(c), w);
+        }
+      });
+      if (blocks > 1) {
+        __syncwarp();
+        tc::cluster_sync();  // every block's part is there
+        // `blocks` neighbouring lanes take one 8-column unit of this block's share: each reads one block's part,
+        // all get the sum, and each writes it to one block
+        const int row_units = a.mp / 8, all = a.mp * row_units;
+        const int u0 = rank * all / blocks, pairs = ((rank + 1) * all / blocks - u0) * blocks;
+        const int peer = tid % blocks;
+        constexpr int kPairs = kSmallSide * kSmallSide / 8 / kSmallThreads;
+        uint4 hi[kPairs], lo[kPairs];
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+          if (k * kSmallThreads >= pairs) break;
+          const int q = tid + k * kSmallThreads, u = u0 + q / blocks, rr = u / row_units, cu = u % row_units;
+          float2 w[4] = {};
+          if (q < pairs) {
+            const uint32_t from = tc::peer_addr(a_addr + (rr * L.part_stride + cu * 8) * 4, peer);
+            const float4 x = tc::peer_load4(from), y = tc::peer_load4(from + 16);
+            w[0] = make_float2(x.x, x.y), w[1] = make_float2(x.z, x.w);
+            w[2] = make_float2(y.x, y.y), w[3] = make_float2(y.z, y.w);
+          }
+          for (int o = 1; o < blocks; o <<= 1)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              w[i].x += __shfl_xor_sync(0xffffffffu, w[i].x, o);
+              w[i].y += __shfl_xor_sync(0xffffffffu, w[i].y, o);
+            }
+          if (q < pairs && rr / 8 == cu)
+            tc::peer_store(tc::peer_addr(tc::smem_addr(&a_diag[rr]), peer), take(w, rr & 7) * (1.f / kXScale));
+          tc::split8(w, hi[k], lo[k]);
+        }
+        __syncwarp();
+        tc::cluster_sync();  // every part has been read: A may take its place
+#pragma unroll
+        for (int k = 0; k < kPairs; ++k) {
+          if (k * kSmallThreads >= pairs) break;
+          const int q = tid + k * kSmallThreads, u = u0 + q / blocks, rr = u / row_units, cu = u % row_units;
+          if (q < pairs) {
+            const uint32_t to = tc::peer_addr(a_addr + (cu >> 3) * row_set + tc::tile_unit(rr, cu & 7), peer);
+            tc::peer_store16(to, hi[k]);
+            tc::peer_store16(to + L.a_set, lo[k]);
+          }
+        }
+        tc::fence_async_cluster();
+        __syncwarp();
+        tc::cluster_sync();
+      }
+      wrote();
+      // P = b A + c A A (x 2^13) over A: (A A)[r][c] = (R R)[r][c] + (d[r] + d[c]) R[r][c] off the diagonal
+      wait_done();
+      all_wrote();
+      const float dr = row_on ? a_diag[r] : 0.f;
+      for_columns(a.mp, 1, [&](int c, float2(&w)[4]) {
+        const uint32_t at = place(c);
+        float2 x[4];
+        get(as, L.a_set, at, x);
+        if ((r >> 3) == (c >> 3)) {
+          float2 y[4] = {w[0], w[1], w[2], w[3]};
+          p_diag[r] = fmaf(kNsC, fmaf(dr, dr, take(y, r & 7) * (1.f / (kXScale * kXScale))), kNsB * dr);
+        }
+        const float4 d0 = *reinterpret_cast<const float4*>(a_diag + c), d1 = *reinterpret_cast<const float4*>(a_diag + c + 4);
+        const float2 dc[4] = {make_float2(d0.x, d0.y), make_float2(d0.z, d0.w), make_float2(d1.x, d1.y),
+                              make_float2(d1.z, d1.w)};
+        constexpr float k = kPScale / kXScale;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 by = __ffma2_rn(dc[i], pair(k * kNsC), pair(k * fmaf(kNsC, dr, kNsB)));
+          w[i] = __ffma2_rn(w[i], pair(k / kXScale * kNsC), __fmul2_rn(x[i], by));
+        }
+        if ((r >> 3) == (c >> 3)) take(w, r & 7);
+        put(as, L.a_set, at, w);
+      });
+      wrote();
+      // X = (a + diagonal of P) X + (the rest of P) X
+      wait_done();
+      all_wrote();
+      const float dx = row_on ? kNsA + p_diag[r] : 0.f;
+      const bool last = step + 1 == a.steps;
+      for_columns(a.nj, 1, [&](int c, float2(&w)[4]) {
+        const uint32_t at = place(c);
+        float2 x[4];
+        get(xs, L.x_set, at, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __ffma2_rn(w[i], pair(1.f / kPScale), __fmul2_rn(x[i], pair(dx)));
+        if (!last) {
+          put(xs, L.x_set, at, w);
+        } else if (r < a.m) {
+          const int col = c0 + c;
+          const float by = ok ? a.scale / kXScale : __int_as_float(0x7fffffff);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = __fmul2_rn(w[i], pair(by));
+          if (a.vec4 && col + 8 <= a.n) {
+            float4* to = reinterpret_cast<float4*>(out + (long long)r * a.cols + col);
+            to[0] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
+            to[1] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
+          } else {
+            const float o[8] = {w[0].x, w[0].y, w[1].x, w[1].y, w[2].x, w[2].y, w[3].x, w[3].y};
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-              w[i] = fmaf(kNsC / (kXScale * kXScale), v[8 * h + i], fmaf(kNsB, w[i], c + 8 * h + i == r ? kNsA : 0.f));
-            tc::split8(w, kPScale, hi, lo);
-            *reinterpret_cast<uint4*>(as + at) = hi;
-            *reinterpret_cast<uint4*>(as + L.a_set + at) = lo;
+              if (col + i < a.n)
+                out[a.tall ? (long long)(col + i) * a.cols + r : (long long)r * a.cols + col + i] = o[i];
           }
         }
+      });
+      if (!last) {
+        wrote();
+        all_wrote();
       }
     }
-    ready();
-    // X = (a + b A + c A A) X
-    if (tid == 0) rows_by_columns();
-    wait();
-    const bool last = step + 1 == a.steps;
-    if (live) {
-      for (int c = half * 16; c < a.nj; c += 32) {
-        float v[16];
-        tc::tmem_load16(t_row + c, v);
-        if (r < a.mp) {
-#pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] *= 1.f / (kXScale * kPScale);
-          if (!last) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const float w[8] = {v[8 * h],     v[8 * h + 1], v[8 * h + 2], v[8 * h + 3],
-                                  v[8 * h + 4], v[8 * h + 5], v[8 * h + 6], v[8 * h + 7]};
-              uint4 hi, lo;
-              tc::split8(w, kXScale, hi, lo);
-              const uint32_t at = (c >> 6) * row_set + tc::tile_unit(r, ((c >> 3) + h) & 7);
-              *reinterpret_cast<uint4*>(xs + at) = hi;
-              *reinterpret_cast<uint4*>(xs + L.x_set + at) = lo;
-            }
-          } else if (r < a.m) {
-            const float bad = __int_as_float(0x7fffffff);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = ok ? v[i] * a.scale : bad;
-            if (a.tall) {
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (c0 + c + i < a.n) out[(long long)(c0 + c + i) * a.cols + r] = v[i];
-            } else if (a.cols % 4 == 0 && (reinterpret_cast<uintptr_t>(a.out) & 15) == 0) {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (c0 + c + 4 * i < a.n)
-                  *reinterpret_cast<float4*>(out + (long long)r * a.cols + c0 + c + 4 * i) =
-                      make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                if (c0 + c + i < a.n) out[(long long)r * a.cols + c0 + c + i] = v[i];
-            }
-          }
-        }
-      }
-    }
-    ready();
   }
-  if (warp == 0) tc::tmem_free(tmem, columns);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (issuer) tc::tmem_free(tmem, columns);
   if (blocks > 1) tc::cluster_sync();  // no block leaves while another may still read its shared memory
 }
 
@@ -414,6 +519,12 @@ cudaError_t launch_small(int batch, int rows, int cols, int steps, float scale, 
   const int blocks = small_blocks(a.m, a.n);
   a.mp = (a.m + 15) / 16 * 16;
   a.nj = ((a.n + blocks - 1) / blocks + 15) / 16 * 16;
+  // Sums of like signs (the diagonal) lose half a step each time 16 columns are
+  // added: accumulators of some 64 columns, added in fp32, keep that small.  256
+  // columns of tensor memory at most, so that two blocks fit an SM.
+  a.parts = a.nj / 64 < 256 / a.mp ? a.nj / 64 : 256 / a.mp;
+  a.parts = a.parts < 1 ? 1 : a.parts > 4 ? 4 : a.parts;
+  a.vec4 = !a.tall && cols % 4 == 0 && (((uintptr_t)g | (uintptr_t)out) & 15u) == 0;
   a.scale = scale;
   a.g = g;
   a.out = out;
@@ -422,7 +533,7 @@ cudaError_t launch_small(int batch, int rows, int cols, int steps, float scale, 
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)batch * blocks);
-  cfg.blockDim = dim3(kSmallThreads);
+  cfg.blockDim = dim3(kSmallThreads + 32);
   cfg.dynamicSmemBytes = bytes;
   cfg.stream = stream;
   cudaLaunchAttribute attr{};

@@ -44,7 +44,8 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity) {
 
 // ---- ordering between the generic proxy (ordinary loads and stores), the
 // async proxy (tensor-core and TMA accesses of shared memory) and tcgen05
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void fence_async_cluster() { asm volatile("fence.proxy.async;" ::: "memory"); }
 __device__ __forceinline__ void fence_before_sync() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -57,18 +58,22 @@ __device__ __forceinline__ void tmem_alloc(uint32_t smem_slot, uint32_t columns)
 __device__ __forceinline__ void tmem_free(uint32_t tmem, uint32_t columns) {
   asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(columns));
 }
-// 16 consecutive fp32 columns of the warp's 32 lanes (one row a thread)
-__device__ __forceinline__ void tmem_load16(uint32_t addr, float (&v)[16]) {
-  uint32_t r[16];
+// 16 consecutive fp32 columns of the warp's 32 lanes (one row a thread); the
+// values are there after tmem_wait, which may follow several loads.
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
       "[%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+}
+__device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+               :
+               : "memory");
 }
 
 // ---- operands: tiles of rows x 64 fp16 (128 bytes a row), 128-byte swizzle
@@ -88,17 +93,35 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t columns) {
 __device__ __forceinline__ uint32_t instruction(int n, bool b_mn_major) {
   return (1u << 4) | (b_mn_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) | ((128u >> 4) << 24);
 }
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+// One lane of a converged warp (the same one each time).
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t lane;
   asm volatile(
       "{\n.reg .pred p;\n"
+      "elect.sync _|p, 0xffffffff;\n"
+      "selp.b32 %0, 1, 0, p;\n}\n"
+      : "=r"(lane));
+  return lane;
+}
+// Issued by the lane with `issue` set.  The whole warp runs the code around it,
+// so that descriptors stay in uniform registers.
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool accumulate, uint32_t issue) {
+  asm volatile(
+      "{\n.reg .pred p, q;\n"
       "setp.ne.b32 p, %4, 0;\n"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate)
+      "setp.ne.b32 q, %5, 0;\n"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)accumulate), "r"(issue)
       : "memory");
 }
-// Arrives on the mbarrier when every MMA issued so far by this thread is done.
-__device__ __forceinline__ void commit(uint32_t bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+// Arrives on the mbarrier when every MMA issued so far by this lane is done.
+__device__ __forceinline__ void commit(uint32_t bar, uint32_t issue) {
+  asm volatile(
+      "{\n.reg .pred q;\n"
+      "setp.ne.b32 q, %1, 0;\n"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(issue)
+      : "memory");
 }
 
 // ---- clusters: every block of the cluster arrives, then waits
@@ -123,36 +146,34 @@ __device__ __forceinline__ double peer_load_double(uint32_t addr) {
   asm volatile("ld.shared::cluster.f64 %0, [%1];" : "=d"(v) : "r"(addr) : "memory");
   return v;
 }
+__device__ __forceinline__ void peer_store(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
 __device__ __forceinline__ void peer_store16(uint32_t addr, uint4 v) {
   asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                : "memory");
 }
 
-// ---- fp32 as a pair of fp16: x 2^k = high + low with |x 2^k - high - low| <= 2^-22 |x 2^k|.
-// Eight values make one 16-byte unit of each tile.
-__device__ __forceinline__ void split8(const float (&x)[8], float scale, uint4& high, uint4& low) {
+// ---- fp32 as a pair of fp16: x = high + low with |x - high - low| <= 2^-22 |x| for x
+// scaled into the upper range of fp16.  Eight values make one 16-byte unit of each tile.
+__device__ __forceinline__ void split8(const float2 (&x)[4], uint4& high, uint4& low) {
   uint32_t h[4], l[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float a = x[2 * i] * scale, b = x[2 * i + 1] * scale;
-    const __half2 hi = __floats2half2_rn(a, b);
-    const float2 back = __half22float2(hi);
-    const __half2 lo = __floats2half2_rn(a - back.x, b - back.y);
+    const __half2 hi = __float22half2_rn(x[i]);
+    const __half2 lo = __float22half2_rn(__ffma2_rn(__half22float2(hi), make_float2(-1.f, -1.f), x[i]));
     h[i] = *reinterpret_cast<const uint32_t*>(&hi);
     l[i] = *reinterpret_cast<const uint32_t*>(&lo);
   }
   high = make_uint4(h[0], h[1], h[2], h[3]);
   low = make_uint4(l[0], l[1], l[2], l[3]);
 }
-__device__ __forceinline__ void join8(const uint4& high, const uint4& low, float scale, float (&x)[8]) {
+__device__ __forceinline__ void join8(const uint4& high, const uint4& low, float2 (&x)[4]) {
   const uint32_t h[4] = {high.x, high.y, high.z, high.w}, l[4] = {low.x, low.y, low.z, low.w};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
-    const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&l[i]));
-    x[2 * i] = (a.x + b.x) * scale;
-    x[2 * i + 1] = (a.y + b.y) * scale;
-  }
+  for (int i = 0; i < 4; ++i)
+    x[i] = __fadd2_rn(__half22float2(*reinterpret_cast<const __half2*>(&h[i])),
+                      __half22float2(*reinterpret_cast<const __half2*>(&l[i])));
 }
 
 }  // namespace tc
