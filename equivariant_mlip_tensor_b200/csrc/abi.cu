@@ -1204,7 +1204,7 @@ cgtp_status cgtp_group_norm_backward(int n, int n_samples, int channels, int gro
 }
 
 cgtp_status cgtp_orthogonalise_workspace_size(int batch, int rows, int cols, size_t* bytes) {
-  if (batch < 0 || rows < 0 || cols < 0 || batch > 65535 || rows > 65536 || cols > 65536 || bytes == nullptr)
+  if (batch < 0 || rows < 0 || cols < 0 || batch > 65535 || rows > 8192 || cols > 8192 || bytes == nullptr)
     return CGTP_ERR_INVALID_ARG;
   *bytes = batch == 0 || rows == 0 || cols == 0 ? 0 : ortho_workspace(batch, rows, cols);
   return CGTP_OK;

@@ -20,6 +20,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "common.cuh"
 #include "tc.cuh"
 #include "train_ops.h"
 
@@ -28,74 +29,6 @@ namespace {
 
 constexpr float kNsA = 3.4445f, kNsB = -4.7750f, kNsC = 2.0315f;
 constexpr double kNsEps = 1e-7;
-
-// One block per matrix: X [m][n] (m <= n) = G / (|G|_F + eps).  The squares are
-// summed in 64 bits: they can neither overflow nor vanish.
-__global__ void __launch_bounds__(512) ortho_start_kernel(int rows, int cols, const float* __restrict__ g,
-                                                           float* __restrict__ x) {
-  __shared__ double red[512];
-  const long long size = (long long)rows * cols;
-  g += blockIdx.x * size;
-  x += blockIdx.x * size;
-  double s = 0.0;
-  for (long long i = threadIdx.x; i < size; i += 512) s += (double)g[i] * g[i];
-  red[threadIdx.x] = s;
-  __syncthreads();
-  for (int o = 256; o > 0; o >>= 1) {
-    if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
-    __syncthreads();
-  }
-  const double inv = 1.0 / (sqrt(red[0]) + kNsEps);
-  for (long long i = threadIdx.x; i < size; i += 512) {
-    const long long r = i / cols, c = i % cols;
-    x[rows > cols ? c * rows + r : i] = (float)(g[i] * inv);
-  }
-}
-
-// d = alpha a b + beta e for a stack of matrices, 64 x 64 tiles; B_T: b is
-// given transposed.  OUT_T: d is written transposed and scaled.
-constexpr int kTile = 64, kDepth = 16;
-template <bool B_T>
-__global__ void __launch_bounds__(256)
-    ortho_product_kernel(int m, int n, int k, const float* __restrict__ a, const float* __restrict__ b, float alpha,
-                         float beta, const float* __restrict__ e, float scale, int out_t, float* __restrict__ d) {
-  __shared__ float as[kDepth][kTile + 4], bs[kDepth][kTile + 4];
-  const long long z = blockIdx.z;
-  a += z * m * k;
-  b += z * n * k;
-  e += z * m * n;
-  d += z * m * n;
-  const int m0 = blockIdx.y * kTile, n0 = blockIdx.x * kTile;
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < k; k0 += kDepth) {
-    for (int i = threadIdx.x; i < kTile * kDepth; i += 256) {
-      const int r = i / kDepth, q = i % kDepth;
-      as[q][r] = m0 + r < m && k0 + q < k ? a[(long long)(m0 + r) * k + k0 + q] : 0.f;
-      if (B_T) bs[q][r] = n0 + r < n && k0 + q < k ? b[(long long)(n0 + r) * k + k0 + q] : 0.f;
-    }
-    if (!B_T)
-      for (int i = threadIdx.x; i < kTile * kDepth; i += 256) {
-        const int q = i / kTile, r = i % kTile;
-        bs[q][r] = n0 + r < n && k0 + q < k ? b[(long long)(k0 + q) * n + n0 + r] : 0.f;
-      }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < kDepth; ++q)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[q][ty * 4 + i], bs[q][tx * 4 + j], acc[i][j]);
-    __syncthreads();
-  }
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int r = m0 + ty * 4 + i, c = n0 + tx * 4 + j;
-      if (r < m && c < n)
-        d[out_t ? (long long)c * m + r : (long long)r * n + c] =
-            scale * fmaf(alpha, acc[i][j], beta == 0.f ? 0.f : beta * e[(long long)r * n + c]);
-    }
-}
 
 // ---------------------------------------------------------- the short side up to 128
 // All steps of one matrix in one launch: a cluster of 1, 2, 4 or 8 blocks holds
@@ -547,38 +480,381 @@ cudaError_t launch_small(int batch, int rows, int cols, int steps, float scale, 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// ------------------------------------------------------------- larger matrices
+// One launch per product, over 128 x 128 tiles of the result.  X, A and P lie in
+// the workspace as the operands' own shared-memory tiles (128 rows x 64 columns
+// of fp16, swizzled, 16 KB; the low parts a set of tiles behind the high ones),
+// so a tile is one bulk copy, and the tiles that X X^T reads along their rows
+// P X reads down them.  Rows and columns beyond the matrix are zero and stay so.
+// A block has one warp that copies (kStages stages of 64 columns), one that
+// issues the products and sixteen that turn the accumulator into the next
+// operand.  The launches are dependent ones (programmatic stream serialization):
+// each sets up while the one before ends and waits for it before its first
+// access to global memory.  Four accumulators fill the tensor memory: one for low high + high
+// low, three that share the columns of high high, so that no entry is rounded
+// towards zero more often than once in 48 columns (2 x 1024 x 1024, one
+// accumulator for all but X X^T: 4.9e-6 of the result, with four: FIXME).
+constexpr int kTileBytes = 128 * 128, kStages = 3, kStageBytes = 4 * kTileBytes;
+constexpr int kLargeThreads = kSmallThreads + 64;
+constexpr int kLargeParts = 3;
+
+struct LargeArgs {
+  int rows, cols, m, n, tall, vec4;
+  int mt, kt, nt;  // tiles: rows of X (128), columns of A with data (64), columns of X (64, even)
+  float scale;
+  long long x_set, a_set;  // bytes of one set of tiles of one matrix
+  uint8_t *x, *x_next, *a, *p;  // [batch][2 sets][row tiles][column tiles]
+  float *a_diag, *p_diag;       // [batch][mt * 128]
+  double* sums;                 // [batch][kSumBlocks] sums of squares
+  const float* g;
+  float* out;
+};
+constexpr int kSumBlocks = 64;
+
+// Sums of squares of a matrix, in 64 bits, one per block.
+__global__ void __launch_bounds__(256) ortho_norm_kernel(LargeArgs a) {
+  grid_dependents_launch();
+  __shared__ double red[256];
+  const long long size = (long long)a.rows * a.cols;
+  const float* g = a.g + blockIdx.y * size;
+  double s = 0.0;
+#pragma unroll 4
+  for (long long i = blockIdx.x * 256 + threadIdx.x; i < size; i += kSumBlocks * 256) s = fma((double)g[i], (double)g[i], s);
+  red[threadIdx.x] = s;
+  __syncthreads();
+  for (int o = 128; o > 0; o >>= 1) {
+    if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) a.sums[(long long)blockIdx.y * kSumBlocks + blockIdx.x] = red[0];
+}
+
+// 2^14 X as tiles: one block per tile.
+__global__ void __launch_bounds__(256) ortho_tiles_kernel(LargeArgs a) {
+  const int ct = blockIdx.x, rt = blockIdx.y, z = blockIdx.z;
+  grid_dependents_launch();
+  grid_dependency_wait();
+  double s = 0.0;
+  for (int k = 0; k < kSumBlocks; ++k) s += a.sums[(long long)z * kSumBlocks + k];
+  int e;
+  const float f = (float)frexp(kXScale / (sqrt(s) + kNsEps), &e);
+  const float s1 = ldexpf(1.f, e / 2), s2 = ldexpf(f, e - e / 2);
+  const float* g = a.g + (long long)z * a.rows * a.cols;
+  uint8_t* to = a.x + (2 * z * a.x_set) + ((long long)rt * a.nt + ct) * kTileBytes;
+  for (int q = threadIdx.x; q < 128 * 8; q += 256) {
+    const int r = a.tall ? q & 127 : q >> 3, u = a.tall ? q >> 7 : q & 7;
+    const int row = rt * 128 + r, col = ct * 64 + u * 8;
+    float2 w[4];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      float v = 0.f;
+      if (row < a.m && col + i < a.n)
+        v = g[a.tall ? (long long)(col + i) * a.cols + row : (long long)row * a.cols + col + i] * s1 * s2;
+      if (i & 1) w[i / 2].y = v;
+      else w[i / 2].x = v;
+    }
+    uint4 hi, lo;
+    tc::split8(w, hi, lo);
+    const uint32_t at = tc::tile_unit(r, u);
+    *reinterpret_cast<uint4*>(to + at) = hi;
+    *reinterpret_cast<uint4*>(to + a.x_set + at) = lo;
+  }
+}
+
+enum { kGram = 0, kSquare = 1, kApply = 2 };
+
+// kGram: A = X X^T.  kSquare: P = b A + c A A.  kApply: X' = (a + P) X, or the output when LAST.
+template <int MODE, bool LAST>
+__global__ void __launch_bounds__(kLargeThreads, 1) ortho_product_kernel(LargeArgs a) {
+  grid_dependents_launch();
+  extern __shared__ uint8_t raw[];
+  __shared__ uint32_t tmem_slot;
+  __shared__ uint64_t bars[2 * kStages + 1];
+  uint8_t* base = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
+  const uint32_t smem = tc::smem_addr(base);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int ct = blockIdx.x, rt = blockIdx.y;  // tile of the result, 128 columns wide
+  const long long z = blockIdx.z;
+  uint8_t* xz = a.x + 2 * z * a.x_set;
+  uint8_t* az = a.a + 2 * z * a.a_set;
+  uint8_t* pz = a.p + 2 * z * a.a_set;
+  const int at_cols = 2 * a.mt;  // column tiles of A
+  const int chunks = MODE == kGram ? (a.n + 63) / 64 : a.kt;
+  constexpr int kColumns = 128 * (kLargeParts + 1);
+  const int parts = chunks < kLargeParts ? chunks : kLargeParts;
+  auto full = [&](int s) { return tc::smem_addr(&bars[s]); };
+  auto empty = [&](int s) { return tc::smem_addr(&bars[kStages + s]); };
+  const uint32_t done = tc::smem_addr(&bars[2 * kStages]);
+
+  if (warp == kSmallThreads / 32) {
+    tc::tmem_alloc(tc::smem_addr(&tmem_slot), kColumns);
+    if (lane == 0)
+      for (int k = 0; k < 2 * kStages + 1; ++k) tc::mbar_init(tc::smem_addr(&bars[k]), 1);
+  }
+  tc::fence_async();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  bool ok = true;
+  grid_dependency_wait();
+
+  if (warp == kSmallThreads / 32 + 1) {
+    if (lane == 0) {  // copies
+      for (int c = 0; c < chunks && ok; ++c) {
+        const int s = c % kStages;
+        if (c >= kStages) ok = tc::mbar_wait(empty(s), (c / kStages - 1) & 1);
+        if (!ok) break;
+        const uint32_t to = smem + s * kStageBytes;
+        tc::mbar_expect(full(s), kStageBytes);
+#pragma unroll
+        for (int set = 0; set < 2; ++set) {
+          const uint8_t* left = MODE == kGram    ? xz + set * a.x_set + ((long long)rt * a.nt + c) * kTileBytes
+                                : MODE == kSquare ? az + set * a.a_set + ((long long)rt * at_cols + c) * kTileBytes
+                                                  : pz + set * a.a_set + ((long long)rt * at_cols + c) * kTileBytes;
+          tc::bulk_load(to + set * kTileBytes, left, kTileBytes, full(s));
+          const uint32_t right = to + (2 + set) * kTileBytes;
+          if (MODE == kApply) {  // 64 rows of two column tiles
+            const uint8_t* from = xz + set * a.x_set + ((long long)(c >> 1) * a.nt + 2 * ct) * kTileBytes + (c & 1) * (kTileBytes / 2);
+            tc::bulk_load(right, from, kTileBytes / 2, full(s));
+            tc::bulk_load(right + kTileBytes / 2, from + kTileBytes, kTileBytes / 2, full(s));
+          } else {
+            const uint8_t* from = MODE == kGram ? xz + set * a.x_set + ((long long)ct * a.nt + c) * kTileBytes
+                                                : az + set * a.a_set + ((long long)ct * at_cols + c) * kTileBytes;
+            tc::bulk_load(right, from, kTileBytes, full(s));
+          }
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == kSmallThreads / 32) {  // products
+    const uint32_t issue = tc::elect(), idesc = tc::instruction(128, MODE == kApply);
+    constexpr uint32_t kSet = kTileBytes / 16;  // low parts, in 16-byte units
+    for (int c = 0; c < chunks; ++c) {
+      const int s = c % kStages;
+      if (ok) ok = tc::mbar_wait(full(s), (c / kStages) & 1);
+      tc::fence_after_sync();
+      const uint32_t from = smem + s * kStageBytes;
+      const uint64_t da = tc::desc_k(from);
+      const uint64_t db = MODE == kApply ? tc::desc_mn(from + 2 * kTileBytes, kTileBytes / 2) : tc::desc_k(from + 2 * kTileBytes);
+      constexpr uint32_t kStep = MODE == kApply ? 128 : 2;
+      const int p = c * parts / chunks;
+      const bool fresh = c == 0 || (c - 1) * parts / chunks != p;
+      const uint32_t d = tmem + p * 128, cross = tmem + kLargeParts * 128;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        tc::mma(cross, da + kSet + 2 * i, db + kStep * i, idesc, c > 0 || i > 0, issue);
+        tc::mma(cross, da + 2 * i, db + kSet + kStep * i, idesc, true, issue);
+        tc::mma(d, da + 2 * i, db + kStep * i, idesc, !fresh || i > 0, issue);
+      }
+      tc::commit(empty(s), issue);
+    }
+    tc::commit(done, issue);
+    __syncwarp();
+  } else {
+    const int r = (warp & 3) * 32 + lane, first = (warp >> 2) * 16, row = rt * 128 + r;
+    const uint32_t t_row = tmem + ((uint32_t)((warp & 3) * 32) << 16);
+    const bool diagonal = MODE != kApply && rt == ct;
+    const float* ad = a.a_diag + z * a.mt * 128;
+    float* pd = a.p_diag + z * a.mt * 128;
+    // what the tile's own elements are combined with, read while the products run
+    uint4 own[MODE == kGram ? 1 : 4][2];
+    const uint8_t* from = MODE == kSquare ? az + ((long long)rt * at_cols + 2 * ct) * kTileBytes
+                                          : xz + ((long long)rt * a.nt + 2 * ct) * kTileBytes;
+    const long long set = MODE == kApply ? a.x_set : a.a_set;
+    if (MODE != kGram)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int c = first + (k >> 1) * 64 + (k & 1) * 8;
+        const uint8_t* p = from + (c >> 6) * kTileBytes + tc::tile_unit(r, (c >> 3) & 7);
+        own[k][0] = *reinterpret_cast<const uint4*>(p);
+        own[k][1] = *reinterpret_cast<const uint4*>(p + set);
+      }
+    const float dr = MODE == kSquare ? ad[row] : MODE == kApply ? kNsA + pd[row] : 0.f;
+    ok = tc::mbar_wait(done, 0);
+    tc::fence_after_sync();
+    const float fine = ok ? 1.f : __int_as_float(0x7fffffff);
+    auto pair = [](float v) { return make_float2(v, v); };
+    auto take = [](float2(&w)[4], int col) {
+      float d = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (col == 2 * i) d = w[i].x, w[i].x = 0.f;
+        if (col == 2 * i + 1) d = w[i].y, w[i].y = 0.f;
+      }
+      return d;
+    };
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+      const int c = first + half * 64;
+      uint32_t v[16];
+      tc::tmem_load16(t_row + kLargeParts * 128 + c, v);
+      tc::tmem_wait(v);
+      float2 acc[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[i] = make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+      for (int k = 0; k < parts; ++k) {
+        tc::tmem_load16(t_row + k * 128 + c, v);
+        tc::tmem_wait(v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          acc[i] = __fadd2_rn(acc[i], make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])));
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int cu = c + 8 * h;
+        float2 w[4] = {acc[4 * h], acc[4 * h + 1], acc[4 * h + 2], acc[4 * h + 3]};
+        const bool on_diagonal = diagonal && (r >> 3) == (cu >> 3);
+        if (MODE == kGram) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) w[i] = __fmul2_rn(w[i], pair(fine / kXScale));
+          if (on_diagonal) a.a_diag[z * a.mt * 128 + row] = take(w, r & 7) * (1.f / kXScale);
+        } else {
+          float2 x[4];
+          tc::join8(own[2 * half + h][0], own[2 * half + h][1], x);
+          if (MODE == kSquare) {
+            if (on_diagonal) {
+              float2 y[4] = {w[0], w[1], w[2], w[3]};
+              pd[row] = fmaf(kNsC, fmaf(dr, dr, take(y, r & 7) * (1.f / (kXScale * kXScale))), kNsB * dr);
+            }
+            const float4 d0 = *reinterpret_cast<const float4*>(ad + ct * 128 + cu);
+            const float4 d1 = *reinterpret_cast<const float4*>(ad + ct * 128 + cu + 4);
+            const float2 dc[4] = {make_float2(d0.x, d0.y), make_float2(d0.z, d0.w), make_float2(d1.x, d1.y),
+                                  make_float2(d1.z, d1.w)};
+            constexpr float k = kPScale / kXScale;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 by = __ffma2_rn(dc[i], pair(k * kNsC), pair(k * fmaf(kNsC, dr, kNsB)));
+              w[i] = __ffma2_rn(w[i], pair(fine * (k / kXScale * kNsC)), __fmul2_rn(x[i], by));
+            }
+            if (on_diagonal) take(w, r & 7);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __ffma2_rn(w[i], pair(fine / kPScale), __fmul2_rn(x[i], pair(dr)));
+          }
+        }
+        if (MODE == kApply && LAST) {
+          const int col = ct * 128 + cu;
+          if (row < a.m) {
+            float* out = a.out + z * a.rows * a.cols;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __fmul2_rn(w[i], pair(a.scale / kXScale));
+            if (a.vec4 && col + 8 <= a.n) {
+              float4* to = reinterpret_cast<float4*>(out + (long long)row * a.cols + col);
+              to[0] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
+              to[1] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
+            } else {
+              const float o[8] = {w[0].x, w[0].y, w[1].x, w[1].y, w[2].x, w[2].y, w[3].x, w[3].y};
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (col + i < a.n)
+                  out[a.tall ? (long long)(col + i) * a.cols + row : (long long)row * a.cols + col + i] = o[i];
+            }
+          }
+        } else {  // the stages are free: tile cu / 64, high and low
+          uint4 hi, lo;
+          tc::split8(w, hi, lo);
+          uint8_t* to = base + (cu >> 6) * 2 * kTileBytes + tc::tile_unit(r, (cu >> 3) & 7);
+          *reinterpret_cast<uint4*>(to) = hi;
+          *reinterpret_cast<uint4*>(to + kTileBytes) = lo;
+        }
+      }
+    }
+  }
+  tc::fence_async();
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == kSmallThreads / 32) tc::tmem_free(tmem, kColumns);
+  if (!(MODE == kApply && LAST) && tid == 0) {
+    uint8_t* to = MODE == kGram    ? az + ((long long)rt * at_cols + 2 * ct) * kTileBytes
+                  : MODE == kSquare ? pz + ((long long)rt * at_cols + 2 * ct) * kTileBytes
+                                    : a.x_next + 2 * z * a.x_set + ((long long)rt * a.nt + 2 * ct) * kTileBytes;
+    const long long set = MODE == kApply ? a.x_set : a.a_set;
+    for (int k = 0; k < 4; ++k)
+      tc::bulk_store(to + (k >> 1) * kTileBytes + (k & 1) * set, smem + k * kTileBytes, kTileBytes);
+    tc::bulk_store_wait();
+  }
+}
+
+struct LargeLayout {
+  int mt, kt, nt;
+  size_t x_set, a_set, bytes;
+};
+LargeLayout large_layout(int batch, int m, int n) {
+  LargeLayout L;
+  L.mt = (m + 127) / 128;
+  L.kt = (m + 63) / 64;
+  L.nt = (n + 127) / 128 * 2;
+  L.x_set = (size_t)L.mt * L.nt * kTileBytes;
+  L.a_set = (size_t)L.mt * L.mt * 2 * kTileBytes;
+  L.bytes = (size_t)batch * (4 * L.x_set + 4 * L.a_set + 2 * L.mt * 128 * sizeof(float) + kSumBlocks * sizeof(double));
+  return L;
+}
+
+template <int MODE, bool LAST>
+cudaError_t launch_product(const LargeArgs& a, dim3 grid, cudaStream_t stream) {
+  constexpr int bytes = kStages * kStageBytes + 1024;
+  cudaError_t e = cudaFuncSetAttribute(ortho_product_kernel<MODE, LAST>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  return launch_kernel(ortho_product_kernel<MODE, LAST>, grid, kLargeThreads, bytes, stream, true, a);
+}
+
+cudaError_t launch_large(int batch, int rows, int cols, int steps, float scale, const float* g, float* out, void* ws,
+                         cudaStream_t stream) {
+  LargeArgs a{};
+  a.rows = rows;
+  a.cols = cols;
+  a.tall = rows > cols;
+  a.m = a.tall ? cols : rows;
+  a.n = a.tall ? rows : cols;
+  a.vec4 = !a.tall && cols % 4 == 0 && ((uintptr_t)out & 15u) == 0;
+  const LargeLayout L = large_layout(batch, a.m, a.n);
+  a.mt = L.mt;
+  a.kt = L.kt;
+  a.nt = L.nt;
+  a.scale = scale;
+  a.x_set = (long long)L.x_set;
+  a.a_set = (long long)L.a_set;
+  uint8_t* at = (uint8_t*)ws;
+  a.x = at;
+  a.x_next = at += 2 * batch * L.x_set;
+  a.a = at += 2 * batch * L.x_set;
+  a.p = at += 2 * batch * L.a_set;
+  a.sums = (double*)(at += 2 * batch * L.a_set);
+  a.a_diag = (float*)(a.sums + (size_t)batch * kSumBlocks);
+  a.p_diag = a.a_diag + (size_t)batch * L.mt * 128;
+  a.g = g;
+  a.out = out;
+  ortho_norm_kernel<<<dim3(kSumBlocks, batch), 256, 0, stream>>>(a);
+  cudaError_t e = cudaGetLastError();
+  if (e == cudaSuccess) e = launch_kernel(ortho_tiles_kernel, dim3(L.nt, L.mt, batch), 256, 0, stream, true, a);
+  const dim3 square(L.mt, L.mt, batch), wide(L.nt / 2, L.mt, batch);
+  for (int s = 0; s < steps && e == cudaSuccess; ++s) {
+    e = launch_product<kGram, false>(a, square, stream);
+    if (e == cudaSuccess) e = launch_product<kSquare, false>(a, square, stream);
+    if (e == cudaSuccess)
+      e = s + 1 == steps ? launch_product<kApply, true>(a, wide, stream) : launch_product<kApply, false>(a, wide, stream);
+    uint8_t* t = a.x;
+    a.x = a.x_next;
+    a.x_next = t;
+  }
+  return e;
+}
+
 }  // namespace
 
 size_t ortho_workspace(int batch, int rows, int cols) {
-  const size_t m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
-  if (small_blocks((int)m, (int)n) > 0) return 0;
-  return 2 * pad256(sizeof(float) * batch * m * n) + 2 * pad256(sizeof(float) * batch * m * m);
+  const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
+  return small_blocks(m, n) > 0 ? 0 : pad256(large_layout(batch, m, n).bytes);
 }
 
 cudaError_t launch_ortho(int batch, int rows, int cols, int steps, float scale, const float* g, float* out, void* ws,
                          cudaStream_t stream) {
   if (batch == 0 || rows == 0 || cols == 0) return cudaSuccess;
-  const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
-  if (small_blocks(m, n) > 0) return launch_small(batch, rows, cols, steps, scale, g, out, stream);
-  const size_t xb = pad256(sizeof(float) * (size_t)batch * m * n), ab = pad256(sizeof(float) * (size_t)batch * m * m);
-  float* x[2] = {(float*)ws, (float*)((char*)ws + xb)};
-  float* a = (float*)((char*)ws + 2 * xb);
-  float* p = (float*)((char*)ws + 2 * xb + ab);
-  ortho_start_kernel<<<batch, 512, 0, stream>>>(rows, cols, g, x[0]);
-  cudaError_t e = cudaGetLastError();
-  const unsigned tm = (m + kTile - 1) / kTile, tn = (n + kTile - 1) / kTile;
-  for (int s = 0; s < steps && e == cudaSuccess; ++s) {
-    const bool last = s + 1 == steps;
-    ortho_product_kernel<true><<<dim3(tm, tm, batch), 256, 0, stream>>>(m, m, n, x[0], x[0], 1.f, 0.f, x[0], 1.f, 0, a);
-    ortho_product_kernel<true><<<dim3(tm, tm, batch), 256, 0, stream>>>(m, m, m, a, a, kNsC, kNsB, a, 1.f, 0, p);
-    ortho_product_kernel<false><<<dim3(tn, tm, batch), 256, 0, stream>>>(
-        m, n, m, p, x[0], 1.f, kNsA, x[0], last ? scale : 1.f, last && rows > cols, last ? out : x[1]);
-    float* t = x[0];
-    x[0] = x[1];
-    x[1] = t;
-    e = cudaGetLastError();
-  }
-  return e;
+  if (small_blocks(rows < cols ? rows : cols, rows < cols ? cols : rows) > 0)
+    return launch_small(batch, rows, cols, steps, scale, g, out, stream);
+  return launch_large(batch, rows, cols, steps, scale, g, out, ws, stream);
 }
 
 }  // namespace cgtp

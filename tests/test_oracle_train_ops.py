@@ -80,7 +80,7 @@ def test_host_errors():
     assert L.cgtp_embed_backward_workspace_size(4, -1, ctypes.byref(sz)) == 1
     assert L.cgtp_group_norm_workspace_size(4, 1, 12, 5, ctypes.byref(sz)) == 1   # 12 channels, 5 groups
     assert L.cgtp_group_norm_workspace_size(4, 1, 12, 0, ctypes.byref(sz)) == 1
-    assert L.cgtp_orthogonalise_workspace_size(1, 65537, 4, ctypes.byref(sz)) == 1
+    assert L.cgtp_orthogonalise_workspace_size(1, 8193, 4, ctypes.byref(sz)) == 1
     assert L.cgtp_orthogonalise_workspace_size(65536, 4, 4, ctypes.byref(sz)) == 1
     # token sort: missing and aliased arrays, workspace
     assert L.cgtp_token_sort(4, 4, None, P, other, P, big, None) == 1
