@@ -7,28 +7,40 @@
 //   grad_x = rstd (t - <t> - h <t h>);  grad_gamma = sum gz h;  grad_beta = sum gz
 //
 // Bound by memory: the forward has to read x and write y, the backward to read
-// x and grad_y and write grad_x.
+// x and grad_y and write grad_x.  Samples may have any length (graph offsets
+// on the device), and two splits of the work share that:
 //
-// Samples may have any length (graph offsets on the device), so the rows are
-// cut into tiles of equal length whatever the samples are.  The part of sample
-// s in tile t has the slot t + s of its own: going down the rows, each step
-// moves to the next tile or the next sample, so no two parts share a slot.
-//   1. each tile reduces each of its parts per channel into the part's slot
-//      (forward: mean and sum of squared deviations, two passes over values
-//      held in registers; backward: sums of gz and gz h);
+// Fused: a block, or a cluster of 2, 4 or 8 that cut the sample's rows, owns one
+// sample and one slab of whole groups.  The rows stay in registers between the
+// statistics and the result; rows beyond the registers are read again, which
+// finds them in L2.
+//
+// Tiles, for samples so long that a cluster's few blocks could not draw on the
+// memory: the rows are cut into tiles of equal length whatever the samples are.
+// The part of sample s in tile t has the slot t + s of its own: going down the
+// rows, each step moves to the next tile or the next sample, so no two parts
+// share a slot.
+//   1. each tile reduces each of its parts per channel into the part's slot;
 //   2. one group of threads per (sample, group) joins the slots in order;
 //   3. each tile reads its rows again and writes the result.
+//
+// Statistics are means and sums of squared deviations from a mean, joined as
+// such, in fp32: no sum of squares that an offset could cancel.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "common.cuh"
+#include "tc.cuh"
 #include "train_ops.h"
 
 namespace cgtp {
 namespace {
 
 constexpr int kNormThreads = 256;
+constexpr int kNormWarps = kNormThreads / 32;
 constexpr int kNormRows = 8;  // rows per thread, held in registers
 
+// VEC columns of a row; the packed fp32 operations take two at a time.
 template <int VEC>
 struct Vec {
   float v[VEC];
@@ -52,6 +64,86 @@ __device__ __forceinline__ void store_vec(float* p, const Vec<VEC>& a) {
   if constexpr (VEC == 4) *reinterpret_cast<float4*>(p) = make_float4(a.v[0], a.v[1], a.v[2], a.v[3]);
   else *p = a.v[0];
 }
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> fma(const Vec<VEC>& a, const Vec<VEC>& b, const Vec<VEC>& c) {
+  Vec<VEC> r;
+  if constexpr (VEC == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const float2 q = __ffma2_rn(make_float2(a.v[i], a.v[i + 1]), make_float2(b.v[i], b.v[i + 1]),
+                                  make_float2(c.v[i], c.v[i + 1]));
+      r.v[i] = q.x;
+      r.v[i + 1] = q.y;
+    }
+  } else {
+    r.v[0] = fmaf(a.v[0], b.v[0], c.v[0]);
+  }
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> operator+(const Vec<VEC>& a, const Vec<VEC>& b) {
+  Vec<VEC> r;
+  if constexpr (VEC == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const float2 q = __fadd2_rn(make_float2(a.v[i], a.v[i + 1]), make_float2(b.v[i], b.v[i + 1]));
+      r.v[i] = q.x;
+      r.v[i + 1] = q.y;
+    }
+  } else {
+    r.v[0] = a.v[0] + b.v[0];
+  }
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> operator*(const Vec<VEC>& a, const Vec<VEC>& b) {
+  Vec<VEC> r;
+  if constexpr (VEC == 4) {
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+      const float2 q = __fmul2_rn(make_float2(a.v[i], a.v[i + 1]), make_float2(b.v[i], b.v[i + 1]));
+      r.v[i] = q.x;
+      r.v[i + 1] = q.y;
+    }
+  } else {
+    r.v[0] = a.v[0] * b.v[0];
+  }
+  return r;
+}
+template <int VEC>
+__device__ __forceinline__ Vec<VEC> all(float s) {
+  Vec<VEC> r;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) r.v[i] = s;
+  return r;
+}
+
+// 1 / (1 + exp(-z)) by the hardware's base-2 exponential and reciprocal: off by
+// some (|z| + 3) 2^-24 (1 - s) of itself, and 0 or 1 at the ends.
+__device__ __forceinline__ float sigmoid(float z) {
+  float e, s;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.f + e));
+  return s;
+}
+template <bool SILU, int VEC>
+__device__ __forceinline__ Vec<VEC> activate(const Vec<VEC>& z) {
+  Vec<VEC> s = all<VEC>(1.f);
+  if (SILU)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s.v[i] = sigmoid(z.v[i]);
+  return SILU ? z * s : z;
+}
+// g act'(z)
+template <bool SILU, int VEC>
+__device__ __forceinline__ Vec<VEC> activate_grad(const Vec<VEC>& z, const Vec<VEC>& g) {
+  const Vec<VEC> one = all<VEC>(1.f);
+  Vec<VEC> s = one;
+  if (SILU)
+#pragma unroll
+    for (int i = 0; i < VEC; ++i) s.v[i] = sigmoid(z.v[i]);
+  return SILU ? g * s * fma(z, fma(s, all<VEC>(-1.f), one), one) : g;
+}
 
 // Bounds of sample s, clamped into [0, n].
 __device__ __forceinline__ int2 sample_rows(const NormArgs& a, int s) {
@@ -59,6 +151,314 @@ __device__ __forceinline__ int2 sample_rows(const NormArgs& a, int s) {
   const int lo = min(max(a.ptr[s], 0), a.n);
   return make_int2(lo, min(max(a.ptr[s + 1], lo), a.n));
 }
+
+// The scale, shift, -mean and rstd of a thread's columns in sample s.
+template <int VEC>
+struct Columns {
+  Vec<VEC> gamma, beta, minus_mean, rstd;
+  __device__ __forceinline__ void load_params(const NormArgs& a, int col) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      gamma.v[j] = a.gamma == nullptr ? 1.f : a.gamma[col + j];
+      beta.v[j] = a.beta == nullptr ? 0.f : a.beta[col + j];
+    }
+  }
+  __device__ __forceinline__ void load_stats(const NormArgs& a, int col, int s) {
+    const int cpg = a.channels / a.groups;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const long long k = (long long)s * a.groups + (col + j) / cpg;
+      minus_mean.v[j] = -a.mean[k];
+      rstd.v[j] = a.rstd[k];
+    }
+  }
+  __device__ __forceinline__ Vec<VEC> normalised(const Vec<VEC>& x) const { return (x + minus_mean) * rstd; }
+};
+
+// ------------------------------------------------------------------- fused
+struct Slabs {
+  int lanes;   // threads across a slab's columns (a power of two, at most 32)
+  int groups;  // whole groups of a slab
+  int count;   // slabs
+  int blocks;  // blocks per sample and slab (a cluster)
+};
+constexpr int kSlabColumns = 128;
+
+// What the threads of a block share: column sums by warp, then by column or by group.
+struct FusedShared {
+  float red[2][kNormWarps][kSlabColumns];
+  float col[2][kSlabColumns];
+  float sum[2][kSlabColumns];    // by group: this block's
+  float total[2][kSlabColumns];  // by group: the cluster's
+};
+
+struct Place {
+  int sample, part, lane, ty, nty, c0, columns, groups, col, r0, r1, rows;
+  bool on;
+};
+template <int VEC>
+__device__ __forceinline__ Place place_of(const NormArgs& a, const Slabs& f) {
+  Place p;
+  p.part = blockIdx.x % f.blocks;
+  const int slab = blockIdx.x / f.blocks % f.count, cpg = a.channels / a.groups;
+  p.sample = blockIdx.x / f.blocks / f.count;
+  p.lane = threadIdx.x & (f.lanes - 1);
+  p.ty = threadIdx.x / f.lanes;
+  p.nty = kNormThreads / f.lanes;
+  p.groups = min(f.groups, a.groups - slab * f.groups);
+  p.c0 = slab * f.groups * cpg;
+  p.columns = p.groups * cpg;
+  p.col = p.c0 + p.lane * VEC;
+  p.on = p.lane * VEC < p.columns;
+  const int2 b = sample_rows(a, p.sample);
+  p.rows = b.y - b.x;
+  p.r0 = b.x + (int)((long long)p.rows * p.part / f.blocks);
+  p.r1 = b.x + (int)((long long)p.rows * (p.part + 1) / f.blocks);
+  return p;
+}
+
+// Sums over the rows of a block: lanes of a warp with the same columns, then
+// (in shared memory) the warps, in a fixed order.
+template <int VEC>
+__device__ __forceinline__ void sum_rows(Vec<VEC> v, const Place& p, int lanes, float (*red)[kSlabColumns]) {
+  for (int o = lanes; o < 32; o <<= 1)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) v.v[j] += __shfl_xor_sync(0xffffffffu, v.v[j], o);
+  if ((threadIdx.x & 31) < lanes)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j)
+      if (p.lane * VEC + j < kSlabColumns) red[threadIdx.x >> 5][p.lane * VEC + j] = v.v[j];
+}
+
+// Group sums over the columns (and warps) of red, then over the cluster, into total.
+__device__ __forceinline__ void sum_groups(const Place& p, int cpg, int blocks, const float (*red)[kSlabColumns],
+                                           float* sum, float* total) {
+  __syncthreads();
+  for (int g = threadIdx.x >> 5; g < p.groups; g += kNormWarps) {
+    float s = 0.f;
+    for (int e = threadIdx.x & 31; e < kNormWarps * cpg; e += 32) s += red[e / cpg][g * cpg + e % cpg];
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if ((threadIdx.x & 31) == 0) {
+      sum[g] = s;
+      if (blocks == 1) total[g] = s;
+    }
+  }
+  if (blocks > 1) {
+    __syncwarp();
+    tc::cluster_sync();
+    for (int g = threadIdx.x; g < p.groups; g += kNormThreads) {
+      float s = 0.f;
+      for (int k = 0; k < blocks; ++k) s += tc::peer_load(tc::peer_addr(tc::smem_addr(sum + g), k));
+      total[g] = s;
+    }
+  }
+  __syncthreads();
+}
+
+template <int VEC, bool SILU>
+__global__ void __launch_bounds__(kNormThreads) norm_fused_kernel(NormArgs a, Slabs f) {
+  __shared__ FusedShared sh;
+  const Place p = place_of<VEC>(a, f);
+  const int cpg = a.channels / a.groups, g0 = p.c0 / cpg;
+  if (p.rows == 0) {
+    if (p.part == 0)
+      for (int g = threadIdx.x; g < p.groups; g += kNormThreads) {
+        a.mean[(long long)p.sample * a.groups + g0 + g] = 0.f;
+        a.rstd[(long long)p.sample * a.groups + g0 + g] = 1.f / sqrtf(a.eps);
+      }
+    return;  // every block of the cluster
+  }
+  const int step = p.nty * kNormRows;
+  const bool held = p.r1 - p.r0 <= step;
+  Vec<VEC> v[kNormRows];
+  auto read = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kNormRows; ++i) {
+      const int r = base + p.ty + i * p.nty;
+      v[i] = Vec<VEC>{};
+      if (p.on && r < p.r1) v[i] = load_vec<VEC>(a.x + r * a.x_stride + p.col);
+    }
+  };
+  // this thread's rows: count, mean, squared deviations from it
+  float count = 0.f;
+  Vec<VEC> mean{}, dev{};
+  for (int base = p.r0; base < p.r1; base += step) {
+    read(base);
+    float n = 0.f;
+    Vec<VEC> s{}, d{};
+#pragma unroll
+    for (int i = 0; i < kNormRows; ++i) {
+      n += base + p.ty + i * p.nty < p.r1 ? 1.f : 0.f;
+      s = s + v[i];  // rows that are not there are zero
+    }
+    const Vec<VEC> m = s * all<VEC>(1.f / fmaxf(n, 1.f)), minus = m * all<VEC>(-1.f);
+#pragma unroll
+    for (int i = 0; i < kNormRows; ++i)
+      if (base + p.ty + i * p.nty < p.r1) {
+        const Vec<VEC> q = v[i] + minus;
+        d = fma(q, q, d);
+      }
+    if (n > 0.f) {  // join with the rows before
+      const float sum = count + n;
+      const Vec<VEC> q = m + mean * all<VEC>(-1.f);
+      mean = fma(q, all<VEC>(n / sum), mean);
+      dev = fma(q * q, all<VEC>(count * n / sum), dev + d);
+      count = sum;
+    }
+  }
+  const float all_values = float(p.rows) * float(cpg);
+  sum_rows<VEC>(mean * all<VEC>(p.on ? count : 0.f), p, f.lanes, sh.red[0]);
+  sum_groups(p, cpg, f.blocks, sh.red[0], sh.sum[0], sh.total[0]);
+  Columns<VEC> c;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) c.minus_mean.v[j] = p.on ? -(sh.total[0][(p.lane * VEC + j) / cpg] / all_values) : 0.f;
+  const Vec<VEC> q = mean + c.minus_mean;
+  sum_rows<VEC>(fma(q * q, all<VEC>(p.on ? count : 0.f), dev), p, f.lanes, sh.red[1]);
+  sum_groups(p, cpg, f.blocks, sh.red[1], sh.sum[1], sh.total[1]);
+  if (p.part == 0)
+    for (int g = threadIdx.x; g < p.groups; g += kNormThreads) {
+      const long long k = (long long)p.sample * a.groups + g0 + g;
+      a.mean[k] = sh.total[0][g] / all_values;
+      a.rstd[k] = 1.f / sqrtf(sh.total[1][g] / all_values + a.eps);
+    }
+  if (p.on) {
+    c.load_params(a, p.col);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) c.rstd.v[j] = 1.f / sqrtf(sh.total[1][(p.lane * VEC + j) / cpg] / all_values + a.eps);
+    for (int base = p.r0; base < p.r1; base += step) {
+      if (!held) read(base);
+#pragma unroll
+      for (int i = 0; i < kNormRows; ++i) {
+        const int r = base + p.ty + i * p.nty;
+        if (r < p.r1)
+          store_vec<VEC>(a.y + r * a.y_stride + p.col, activate<SILU>(fma(c.gamma, c.normalised(v[i]), c.beta)));
+      }
+    }
+  }
+  if (f.blocks > 1) {
+    __syncwarp();
+    tc::cluster_sync();  // no block leaves while another may still read its sums
+  }
+}
+
+// slots [sample * blocks + part][channel]: (sum gz, sum gz h) of the block's rows
+template <int VEC, bool SILU>
+__global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_fused_kernel(NormArgs a, Slabs f, float2* __restrict__ slots) {
+  grid_dependents_launch();
+  __shared__ FusedShared sh;
+  const Place p = place_of<VEC>(a, f);
+  const int cpg = a.channels / a.groups;
+  float2* slot = slots + ((long long)p.sample * f.blocks + p.part) * a.channels + p.c0;
+  if (p.rows == 0) {
+    for (int k = threadIdx.x; k < p.columns; k += kNormThreads) slot[k] = make_float2(0.f, 0.f);
+    return;  // every block of the cluster
+  }
+  const int step = p.nty * kNormRows;
+  const bool held = p.r1 - p.r0 <= step;
+  Columns<VEC> c{};
+  if (p.on) {
+    c.load_params(a, p.col);
+    c.load_stats(a, p.col, p.sample);
+  }
+  Vec<VEC> h[kNormRows], gz[kNormRows];
+  auto read = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kNormRows; ++i) {
+      const int r = base + p.ty + i * p.nty;
+      h[i] = Vec<VEC>{};
+      gz[i] = Vec<VEC>{};
+      if (p.on && r < p.r1) {
+        h[i] = load_vec<VEC>(a.x + r * a.x_stride + p.col);
+        gz[i] = load_vec<VEC>(a.grad_y + r * a.gy_stride + p.col);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kNormRows; ++i) {
+      if (base + p.ty + i * p.nty < p.r1) {
+        h[i] = c.normalised(h[i]);
+        gz[i] = activate_grad<SILU>(fma(c.gamma, h[i], c.beta), gz[i]);
+      }
+    }
+  };
+  Vec<VEC> s1{}, s2{};
+  for (int base = p.r0; base < p.r1; base += step) {
+    read(base);
+#pragma unroll
+    for (int i = 0; i < kNormRows; ++i) {
+      s1 = s1 + gz[i];
+      s2 = fma(gz[i], h[i], s2);
+    }
+  }
+  sum_rows<VEC>(s1, p, f.lanes, sh.red[0]);
+  sum_rows<VEC>(s2, p, f.lanes, sh.red[1]);
+  __syncthreads();
+  for (int k = threadIdx.x; k < p.columns; k += kNormThreads) {
+    float x = 0.f, y = 0.f;
+#pragma unroll
+    for (int w = 0; w < kNormWarps; ++w) {
+      x += sh.red[0][w][k];
+      y += sh.red[1][w][k];
+    }
+    slot[k] = make_float2(x, y);
+    const float w = a.gamma == nullptr ? 1.f : a.gamma[p.c0 + k];
+    sh.col[0][k] = w * x;
+    sh.col[1][k] = w * y;
+  }
+  __syncthreads();
+  if (a.grad_x == nullptr) return;  // every block
+  for (int g = threadIdx.x >> 5; g < p.groups; g += kNormWarps) {
+    float x = 0.f, y = 0.f;
+    for (int e = threadIdx.x & 31; e < cpg; e += 32) {
+      x += sh.col[0][g * cpg + e];
+      y += sh.col[1][g * cpg + e];
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      x += __shfl_xor_sync(0xffffffffu, x, o);
+      y += __shfl_xor_sync(0xffffffffu, y, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+      sh.sum[0][g] = sh.total[0][g] = x;
+      sh.sum[1][g] = sh.total[1][g] = y;
+    }
+  }
+  if (f.blocks > 1) {
+    __syncwarp();
+    tc::cluster_sync();
+    for (int g = threadIdx.x; g < 2 * p.groups; g += kNormThreads) {
+      const int q = g >= p.groups, i = g - q * p.groups;
+      float s = 0.f;
+      for (int k = 0; k < f.blocks; ++k) s += tc::peer_load(tc::peer_addr(tc::smem_addr(&sh.sum[q][i]), k));
+      sh.total[q][i] = s;
+    }
+  }
+  __syncthreads();
+  if (p.on) {
+    const float all_values = float(p.rows) * float(cpg);
+    Vec<VEC> m1, m2;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      m1.v[j] = -(sh.total[0][(p.lane * VEC + j) / cpg] / all_values);
+      m2.v[j] = -(sh.total[1][(p.lane * VEC + j) / cpg] / all_values);
+    }
+    for (int base = p.r0; base < p.r1; base += step) {
+      if (!held) read(base);
+#pragma unroll
+      for (int i = 0; i < kNormRows; ++i) {
+        const int r = base + p.ty + i * p.nty;
+        if (r < p.r1)
+          store_vec<VEC>(a.grad_x + r * a.gx_stride + p.col, c.rstd * fma(h[i], m2, fma(c.gamma, gz[i], m1)));
+      }
+    }
+  }
+  if (f.blocks > 1) {
+    __syncwarp();
+    tc::cluster_sync();  // no block leaves while another may still read its sums
+  }
+}
+
+// ------------------------------------------------------------------- tiles
 // The sample that row r belongs to: the last one that starts at or before r
 // (-1: none), found in log2(samples) steps.
 __device__ __forceinline__ int sample_of(const NormArgs& a, int r) {
@@ -112,28 +512,18 @@ __device__ __forceinline__ void sum_row_groups(float (&v)[K], float* red, int ty
   for (int j = 0; j < K; ++j) v[j] = mine[j * kNormThreads];
 }
 
-template <bool SILU>
-__device__ __forceinline__ float act(float z) {
-  return SILU ? z / (1.f + expf(-z)) : z;
-}
-template <bool SILU>
-__device__ __forceinline__ float act_grad(float z) {
-  if (!SILU) return 1.f;
-  const float s = 1.f / (1.f + expf(-z));
-  return s * (1.f + z * (1.f - s));
-}
-
 struct Tile {
-  int lane, ty, nty, r0, r1, col;
+  int lane, ty, nty, r0, r1, col, index;
   bool on;  // the thread has columns
 };
 template <int VEC>
-__device__ __forceinline__ Tile make_tile(const NormArgs& a, int lpr) {
+__device__ __forceinline__ Tile make_tile(const NormArgs& a, int lpr, int index) {
   Tile t;
+  t.index = index;
   t.lane = threadIdx.x & (lpr - 1);
   t.ty = threadIdx.x / lpr;
   t.nty = kNormThreads / lpr;
-  t.r0 = blockIdx.x * (t.nty * kNormRows);
+  t.r0 = index * (t.nty * kNormRows);
   t.r1 = min(a.n - t.r0, t.nty * kNormRows) + t.r0;
   t.col = (blockIdx.y * lpr + t.lane) * VEC;
   t.on = t.col < a.channels;
@@ -145,7 +535,7 @@ template <int VEC>
 __global__ void __launch_bounds__(kNormThreads) norm_part_kernel(NormArgs a, int lpr, float2* __restrict__ slots) {
   __shared__ float red[VEC * kNormThreads];
   __shared__ float mean_of[VEC * 32];
-  const Tile t = make_tile<VEC>(a, lpr);
+  const Tile t = make_tile<VEC>(a, lpr, blockIdx.x);
   Vec<VEC> v[kNormRows];
 #pragma unroll
   for (int i = 0; i < kNormRows; ++i) {
@@ -154,36 +544,36 @@ __global__ void __launch_bounds__(kNormThreads) norm_part_kernel(NormArgs a, int
     if (t.on && r < t.r1) v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
   }
   for_parts(a, t.r0, t.r1, [&](int s, int lo, int hi) {
-    float sum[VEC] = {};
+    Vec<VEC> sum{};
 #pragma unroll
     for (int i = 0; i < kNormRows; ++i) {
       const int r = t.r0 + t.ty + i * t.nty;
-      if (r >= lo && r < hi)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) sum[j] += v[i].v[j];
+      if (r >= lo && r < hi) sum = sum + v[i];
     }
     __syncthreads();
-    sum_row_groups<VEC>(sum, red, t.ty, t.nty);
+    sum_row_groups<VEC>(sum.v, red, t.ty, t.nty);
     if (t.ty == 0)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) mean_of[t.lane * VEC + j] = sum[j] / float(hi - lo);
+      for (int j = 0; j < VEC; ++j) mean_of[t.lane * VEC + j] = sum.v[j] / float(hi - lo);
     __syncthreads();
-    float mean[VEC], dev[VEC] = {};
+    Vec<VEC> mean, dev{};
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) mean[j] = mean_of[t.lane * VEC + j];
+    for (int j = 0; j < VEC; ++j) mean.v[j] = mean_of[t.lane * VEC + j];
+    const Vec<VEC> minus = mean * all<VEC>(-1.f);
 #pragma unroll
     for (int i = 0; i < kNormRows; ++i) {
       const int r = t.r0 + t.ty + i * t.nty;
-      if (r >= lo && r < hi)
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) dev[j] = fmaf(v[i].v[j] - mean[j], v[i].v[j] - mean[j], dev[j]);
+      if (r >= lo && r < hi) {
+        const Vec<VEC> q = v[i] + minus;
+        dev = fma(q, q, dev);
+      }
     }
     __syncthreads();
-    sum_row_groups<VEC>(dev, red, t.ty, t.nty);
+    sum_row_groups<VEC>(dev.v, red, t.ty, t.nty);
     if (t.ty == 0 && t.on)
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
-        slots[((long long)blockIdx.x + s) * a.channels + t.col + j] = make_float2(mean[j], dev[j]);
+        slots[((long long)t.index + s) * a.channels + t.col + j] = make_float2(mean.v[j], dev.v[j]);
   });
 }
 
@@ -252,27 +642,11 @@ __global__ void __launch_bounds__(kNormThreads)
   }
 }
 
-// The scale, shift, mean and rstd of a thread's columns in sample s.
-template <int VEC>
-struct Columns {
-  float gamma[VEC], beta[VEC], mean[VEC], rstd[VEC];
-  __device__ __forceinline__ void load(const NormArgs& a, int col, int s) {
-    const int cpg = a.channels / a.groups;
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const long long k = (long long)s * a.groups + (col + j) / cpg;
-      gamma[j] = a.gamma == nullptr ? 1.f : a.gamma[col + j];
-      beta[j] = a.beta == nullptr ? 0.f : a.beta[col + j];
-      mean[j] = a.mean[k];
-      rstd[j] = a.rstd[k];
-    }
-  }
-};
-
-// 3, forward
+// 3, forward.  The tiles from the last to the first: what step 1 read last is
+// still in L2.
 template <int VEC, bool SILU>
 __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(NormArgs a, int lpr) {
-  const Tile t = make_tile<VEC>(a, lpr);
+  const Tile t = make_tile<VEC>(a, lpr, gridDim.x - 1 - blockIdx.x);
   if (!t.on) return;
   Vec<VEC> v[kNormRows];
 #pragma unroll
@@ -280,19 +654,15 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(NormArgs a, in
     const int r = t.r0 + t.ty + i * t.nty;
     if (r < t.r1) v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
   }
+  Columns<VEC> c;
+  c.load_params(a, t.col);
   for_parts(a, t.r0, t.r1, [&](int s, int lo, int hi) {
-    Columns<VEC> c;
-    c.load(a, t.col, s);
+    c.load_stats(a, t.col, s);
 #pragma unroll
     for (int i = 0; i < kNormRows; ++i) {
       const int r = t.r0 + t.ty + i * t.nty;
-      if (r >= lo && r < hi) {
-        Vec<VEC> o;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j)
-          o.v[j] = act<SILU>(fmaf(c.gamma[j], (v[i].v[j] - c.mean[j]) * c.rstd[j], c.beta[j]));
-        store_vec<VEC>(a.y + r * a.y_stride + t.col, o);
-      }
+      if (r >= lo && r < hi)
+        store_vec<VEC>(a.y + r * a.y_stride + t.col, activate<SILU>(fma(c.gamma, c.normalised(v[i]), c.beta)));
     }
   });
 }
@@ -301,7 +671,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(NormArgs a, in
 template <int VEC, bool SILU>
 __global__ void __launch_bounds__(kNormThreads) norm_bwd_part_kernel(NormArgs a, int lpr, float2* __restrict__ slots) {
   __shared__ float red[2 * VEC * kNormThreads];
-  const Tile t = make_tile<VEC>(a, lpr);
+  const Tile t = make_tile<VEC>(a, lpr, blockIdx.x);
   Vec<VEC> v[kNormRows], g[kNormRows];
 #pragma unroll
   for (int i = 0; i < kNormRows; ++i) {
@@ -313,47 +683,88 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_part_kernel(NormArgs a,
       g[i] = load_vec<VEC>(a.grad_y + r * a.gy_stride + t.col);
     }
   }
+  Columns<VEC> c{};
+  if (t.on) c.load_params(a, t.col);
   for_parts(a, t.r0, t.r1, [&](int s, int lo, int hi) {
-    float sum[2 * VEC] = {};
+    Vec<VEC> s1{}, s2{};
     if (t.on) {
-      Columns<VEC> c;
-      c.load(a, t.col, s);
+      c.load_stats(a, t.col, s);
 #pragma unroll
       for (int i = 0; i < kNormRows; ++i) {
         const int r = t.r0 + t.ty + i * t.nty;
-        if (r >= lo && r < hi)
-#pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            const float h = (v[i].v[j] - c.mean[j]) * c.rstd[j];
-            const float gz = g[i].v[j] * act_grad<SILU>(fmaf(c.gamma[j], h, c.beta[j]));
-            sum[j] += gz;
-            sum[VEC + j] = fmaf(gz, h, sum[VEC + j]);
-          }
+        if (r >= lo && r < hi) {
+          const Vec<VEC> h = c.normalised(v[i]), gz = activate_grad<SILU>(fma(c.gamma, h, c.beta), g[i]);
+          s1 = s1 + gz;
+          s2 = fma(gz, h, s2);
+        }
       }
+    }
+    float sum[2 * VEC];
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      sum[j] = s1.v[j];
+      sum[VEC + j] = s2.v[j];
     }
     __syncthreads();
     sum_row_groups<2 * VEC>(sum, red, t.ty, t.nty);
     if (t.ty == 0 && t.on)
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
-        slots[((long long)blockIdx.x + s) * a.channels + t.col + j] = make_float2(sum[j], sum[VEC + j]);
+        slots[((long long)t.index + s) * a.channels + t.col + j] = make_float2(sum[j], sum[VEC + j]);
   });
 }
 
-// grad_gamma and grad_beta: the sum of every slot (unused ones are zero), 32
-// channels a block.
-__global__ void __launch_bounds__(1024) norm_param_kernel(int rows, int channels, const float2* __restrict__ slots,
-                                                          float* __restrict__ grad_gamma, float* __restrict__ grad_beta) {
+// 3, backward; the order of the tiles as in the forward
+template <int VEC, bool SILU>
+__global__ void __launch_bounds__(kNormThreads)
+    norm_bwd_apply_kernel(NormArgs a, int lpr, const float2* __restrict__ terms) {
+  const Tile t = make_tile<VEC>(a, lpr, gridDim.x - 1 - blockIdx.x);
+  if (!t.on) return;
+  Vec<VEC> v[kNormRows], g[kNormRows];
+#pragma unroll
+  for (int i = 0; i < kNormRows; ++i) {
+    const int r = t.r0 + t.ty + i * t.nty;
+    if (r < t.r1) {
+      v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
+      g[i] = load_vec<VEC>(a.grad_y + r * a.gy_stride + t.col);
+    }
+  }
+  Columns<VEC> c;
+  c.load_params(a, t.col);
+  for_parts(a, t.r0, t.r1, [&](int s, int lo, int hi) {
+    c.load_stats(a, t.col, s);
+    Vec<VEC> m1, m2;
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const float2 m = terms[(long long)s * a.groups + (t.col + j) / (a.channels / a.groups)];
+      m1.v[j] = -m.x;
+      m2.v[j] = -m.y;
+    }
+#pragma unroll
+    for (int i = 0; i < kNormRows; ++i) {
+      const int r = t.r0 + t.ty + i * t.nty;
+      if (r >= lo && r < hi) {
+        const Vec<VEC> h = c.normalised(v[i]), gz = activate_grad<SILU>(fma(c.gamma, h, c.beta), g[i]);
+        store_vec<VEC>(a.grad_x + r * a.gx_stride + t.col, c.rstd * fma(h, m2, fma(c.gamma, gz, m1)));
+      }
+    }
+  });
+}
+
+// -------------------------------------------------------------- parameters
+// Sums of rows of slots per channel, 32 channels a block: rows
+// [y per, (y + 1) per) into row y of `sums`, or into the gradients.
+__global__ void __launch_bounds__(1024)
+    norm_param_kernel(int rows, int per, int channels, const float2* __restrict__ slots, float2* __restrict__ sums,
+                      float* __restrict__ grad_gamma, float* __restrict__ grad_beta) {
+  grid_dependency_wait();
   __shared__ float2 red[32][33];
   const int lane = threadIdx.x & 31, ty = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
+  const long long r0 = (long long)blockIdx.y * per, r1 = min((long long)rows, r0 + per);
   float2 s = make_float2(0.f, 0.f);
   if (c < channels) {
-#pragma unroll 4
-    for (int r = ty; r < rows; r += 32) {
-      const float2 v = slots[(long long)r * channels + c];
-      s.x += v.x;
-      s.y += v.y;
-    }
+#pragma unroll 8
+    for (long long r = r0 + ty; r < r1; r += 32) s = __fadd2_rn(s, slots[r * channels + c]);
   }
   red[ty][lane] = s;
   __syncthreads();
@@ -365,50 +776,33 @@ __global__ void __launch_bounds__(1024) norm_param_kernel(int rows, int channels
   }
   const int k = blockIdx.x * 32 + ty;
   if (lane == 0 && k < channels) {
-    if (grad_beta != nullptr) grad_beta[k] = s.x;
-    if (grad_gamma != nullptr) grad_gamma[k] = s.y;
-  }
-}
-
-// 3, backward
-template <int VEC, bool SILU>
-__global__ void __launch_bounds__(kNormThreads)
-    norm_bwd_apply_kernel(NormArgs a, int lpr, const float2* __restrict__ terms) {
-  const Tile t = make_tile<VEC>(a, lpr);
-  if (!t.on) return;
-  Vec<VEC> v[kNormRows], g[kNormRows];
-#pragma unroll
-  for (int i = 0; i < kNormRows; ++i) {
-    const int r = t.r0 + t.ty + i * t.nty;
-    if (r < t.r1) {
-      v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
-      g[i] = load_vec<VEC>(a.grad_y + r * a.gy_stride + t.col);
+    if (sums != nullptr) {
+      sums[(long long)blockIdx.y * channels + k] = s;
+    } else {
+      if (grad_beta != nullptr) grad_beta[k] = s.x;
+      if (grad_gamma != nullptr) grad_gamma[k] = s.y;
     }
   }
-  for_parts(a, t.r0, t.r1, [&](int s, int lo, int hi) {
-    Columns<VEC> c;
-    c.load(a, t.col, s);
-    float2 m[VEC];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j)
-      m[j] = terms[(long long)s * a.groups + (t.col + j) / (a.channels / a.groups)];
-#pragma unroll
-    for (int i = 0; i < kNormRows; ++i) {
-      const int r = t.r0 + t.ty + i * t.nty;
-      if (r >= lo && r < hi) {
-        Vec<VEC> o;
-#pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          const float h = (v[i].v[j] - c.mean[j]) * c.rstd[j];
-          const float gz = g[i].v[j] * act_grad<SILU>(fmaf(c.gamma[j], h, c.beta[j]));
-          o.v[j] = c.rstd[j] * (fmaf(c.gamma[j], gz, -m[j].x) - h * m[j].y);
-        }
-        store_vec<VEC>(a.grad_x + r * a.gx_stride + t.col, o);
-      }
-    }
-  });
+}
+constexpr int kParamRows = 1024, kParamParts = 64;
+
+cudaError_t sum_params(const NormArgs& a, long long rows, const float2* slots, float2* sums, cudaStream_t stream) {
+  if (a.grad_gamma == nullptr && a.grad_beta == nullptr) return cudaSuccess;
+  const unsigned columns = (unsigned)((a.channels + 31) / 32);
+  cudaError_t e = cudaSuccess;
+  if (rows > kParamRows) {
+    const int per = (int)((rows + kParamParts - 1) / kParamParts);
+    e = launch_kernel(norm_param_kernel, dim3(columns, kParamParts), dim3(1024), 0, stream, true, (int)rows, per,
+                      a.channels, slots, sums, (float*)nullptr, (float*)nullptr);
+    if (e != cudaSuccess) return e;
+    slots = sums;
+    rows = kParamParts;
+  }
+  return launch_kernel(norm_param_kernel, dim3(columns), dim3(1024), 0, stream, true, (int)rows, (int)rows, a.channels,
+                       slots, (float2*)nullptr, a.grad_gamma, a.grad_beta);
 }
 
+// ---------------------------------------------------------------- launching
 int lanes_per_row(int width, int vec) {
   const int need = (width + vec - 1) / vec;
   int l = 1;
@@ -418,6 +812,62 @@ int lanes_per_row(int width, int vec) {
 int rows_per_tile(int channels, int vec) { return kNormRows * (kNormThreads / lanes_per_row(channels, vec)); }
 long long tiles_of(int n, int rows) { return ((long long)n + rows - 1) / rows; }
 bool vec4_rows(const void* p, long long stride) { return stride % 4 == 0 && ((uintptr_t)p & 15u) == 0; }
+
+// The fused split for these sizes, or count = 0 for the tiles.  The longest
+// sample is the caller's bound, else four times the average is expected.
+// Slabs are as wide as still lets the registers hold such a sample and gives
+// every SM a block, down to one 32-byte sector a row; then the rows are cut over a
+// cluster, as long as that leaves a block some rows to work on.
+constexpr long long kFewBlocks = 148, kManyBlocks = 8 * kFewBlocks;
+template <int VEC>
+Slabs fused_slabs(const NormArgs& a, int max_rows) {
+  Slabs f{};
+  const int cpg = a.channels / a.groups;
+  const int most = VEC == 4 ? kSlabColumns : 32;  // 32 lanes across
+  if (a.n == 0 || cpg > most) return f;
+  // slabs start on a vector: their groups are a multiple of this
+  int unit = 1;
+  while (unit * cpg % VEC != 0) ++unit;
+  if (unit * cpg > most) return f;
+  long long rows = max_rows > 0 && max_rows < a.n ? max_rows : a.n;
+  if (max_rows <= 0 && a.samples > 1) {
+    const long long expected = 4LL * a.n / a.samples + 64;
+    if (expected < rows) rows = expected;
+  }
+  auto set = [&](int groups) {
+    f.groups = groups < a.groups ? groups : a.groups;
+    f.count = (a.groups + f.groups - 1) / f.groups;
+    f.lanes = lanes_per_row(f.groups * cpg, VEC);
+  };
+  auto held = [&]() { return (long long)kNormRows * (kNormThreads / f.lanes); };
+  set(most / (unit * cpg) * unit);
+  while (f.groups > unit && f.groups * cpg > 8 && (held() < rows || (long long)a.samples * f.count < kFewBlocks)) {
+    const int half = (f.groups / unit + 1) / 2 * unit;
+    if (half == f.groups) break;
+    set(half);
+  }
+  f.blocks = 1;
+  while (f.blocks < 8 && held() * f.blocks < rows && (long long)a.samples * f.count * f.blocks * 2 <= kManyBlocks) f.blocks *= 2;
+  // a block that reads its rows again and again while others are done: leave that to the tiles
+  if (held() * f.blocks * 16 < rows || (long long)a.samples * f.count * f.blocks > 0x7fffffffLL) f.count = 0;
+  return f;
+}
+
+template <class... P, class... A>
+cudaError_t launch_cluster(void (*kernel)(P...), const NormArgs& a, const Slabs& f, cudaStream_t stream, A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)((long long)a.samples * f.count * f.blocks));
+  cfg.blockDim = dim3(kNormThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = f.blocks;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = f.blocks > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, a, f, args...);
+}
 
 template <bool BWD>
 cudaError_t join(const NormArgs& a, int rows, const float2* slots, float2* terms, cudaStream_t stream) {
@@ -432,7 +882,9 @@ cudaError_t join(const NormArgs& a, int rows, const float2* slots, float2* terms
 }
 
 template <int VEC, bool SILU>
-cudaError_t norm_fwd(const NormArgs& a, void* ws, cudaStream_t stream) {
+cudaError_t norm_fwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t stream) {
+  const Slabs f = fused_slabs<VEC>(a, max_rows);
+  if (f.count > 0) return launch_cluster(norm_fused_kernel<VEC, SILU>, a, f, stream);
   const int lpr = lanes_per_row(a.channels, VEC), rows = rows_per_tile(a.channels, VEC);
   const dim3 grid((unsigned)tiles_of(a.n, rows), (unsigned)((a.channels + lpr * VEC - 1) / (lpr * VEC)));
   cudaError_t e = cudaSuccess;
@@ -448,56 +900,63 @@ cudaError_t norm_fwd(const NormArgs& a, void* ws, cudaStream_t stream) {
   return e;
 }
 
+// Workspace: terms, partial sums of the parameters, slots.
+size_t terms_bytes(const NormArgs& a) { return pad256(sizeof(float2) * (size_t)a.samples * a.groups); }
+size_t sums_bytes(const NormArgs& a) { return pad256(sizeof(float2) * (size_t)kParamParts * a.channels); }
+
 template <int VEC, bool SILU>
-cudaError_t norm_bwd(const NormArgs& a, void* ws, cudaStream_t stream) {
+cudaError_t norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t stream) {
+  float2* terms = (float2*)ws;
+  float2* sums = (float2*)((char*)ws + terms_bytes(a));
+  float2* slots = (float2*)((char*)ws + terms_bytes(a) + sums_bytes(a));
+  const Slabs f = fused_slabs<VEC>(a, max_rows);
+  if (f.count > 0 && a.samples > 0) {
+    const cudaError_t e = launch_cluster(norm_bwd_fused_kernel<VEC, SILU>, a, f, stream, slots);
+    return e != cudaSuccess ? e : sum_params(a, (long long)a.samples * f.blocks, slots, sums, stream);
+  }
   const int lpr = lanes_per_row(a.channels, VEC), rows = rows_per_tile(a.channels, VEC);
   const long long tiles = tiles_of(a.n, rows), n_slots = tiles + a.samples;
   const dim3 grid((unsigned)tiles, (unsigned)((a.channels + lpr * VEC - 1) / (lpr * VEC)));
-  float2* terms = (float2*)ws;
-  float2* slots = (float2*)((char*)ws + pad256(sizeof(float2) * (size_t)a.samples * a.groups));
   cudaError_t e = cudaMemsetAsync(slots, 0, sizeof(float2) * (size_t)n_slots * a.channels, stream);
   if (e == cudaSuccess && a.n > 0) {
     norm_bwd_part_kernel<VEC, SILU><<<grid, kNormThreads, 0, stream>>>(a, lpr, slots);
     e = cudaGetLastError();
   }
-  if (e == cudaSuccess && a.grad_x != nullptr) {
+  if (e == cudaSuccess && a.grad_x != nullptr && a.samples > 0) {
     e = join<true>(a, rows, slots, terms, stream);
     if (e == cudaSuccess && a.n > 0) {
       norm_bwd_apply_kernel<VEC, SILU><<<grid, kNormThreads, 0, stream>>>(a, lpr, terms);
       e = cudaGetLastError();
     }
   }
-  if (e == cudaSuccess && (a.grad_gamma != nullptr || a.grad_beta != nullptr)) {
-    norm_param_kernel<<<(a.channels + 31) / 32, 1024, 0, stream>>>((int)n_slots, a.channels, slots, a.grad_gamma,
-                                                                   a.grad_beta);
-    e = cudaGetLastError();
-  }
-  return e;
+  return e != cudaSuccess ? e : sum_params(a, n_slots, slots, sums, stream);
 }
 
 }  // namespace
 
-// Enough for both directions and for rows of any alignment.
+// Enough for both directions, both splits and rows of any alignment.
 size_t norm_workspace(int n, int samples, int channels, int groups) {
-  const size_t slots = (size_t)tiles_of(n, rows_per_tile(channels, 1)) + (size_t)samples;
-  return pad256(sizeof(float2) * (size_t)samples * groups) + pad256(sizeof(float2) * slots * (size_t)channels);
+  NormArgs a{};
+  a.samples = samples;
+  a.channels = channels;
+  a.groups = groups;
+  const size_t slots = (size_t)tiles_of(n, rows_per_tile(channels, 1)) + (size_t)samples + (size_t)kManyBlocks;
+  return terms_bytes(a) + sums_bytes(a) + pad256(sizeof(float2) * slots * (size_t)channels);
 }
 
 cudaError_t launch_norm_fwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t stream) {
-  (void)max_rows;
   if (a.samples == 0 || a.channels == 0) return cudaSuccess;
   const bool v4 = a.channels % 4 == 0 && vec4_rows(a.x, a.x_stride) && vec4_rows(a.y, a.y_stride);
-  if (v4) return a.act ? norm_fwd<4, true>(a, ws, stream) : norm_fwd<4, false>(a, ws, stream);
-  return a.act ? norm_fwd<1, true>(a, ws, stream) : norm_fwd<1, false>(a, ws, stream);
+  if (v4) return a.act ? norm_fwd<4, true>(a, max_rows, ws, stream) : norm_fwd<4, false>(a, max_rows, ws, stream);
+  return a.act ? norm_fwd<1, true>(a, max_rows, ws, stream) : norm_fwd<1, false>(a, max_rows, ws, stream);
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t stream) {
-  (void)max_rows;
   if (a.channels == 0) return cudaSuccess;
   const bool v4 = a.channels % 4 == 0 && vec4_rows(a.x, a.x_stride) && vec4_rows(a.grad_y, a.gy_stride) &&
                   (a.grad_x == nullptr || vec4_rows(a.grad_x, a.gx_stride));
-  if (v4) return a.act ? norm_bwd<4, true>(a, ws, stream) : norm_bwd<4, false>(a, ws, stream);
-  return a.act ? norm_bwd<1, true>(a, ws, stream) : norm_bwd<1, false>(a, ws, stream);
+  if (v4) return a.act ? norm_bwd<4, true>(a, max_rows, ws, stream) : norm_bwd<4, false>(a, max_rows, ws, stream);
+  return a.act ? norm_bwd<1, true>(a, max_rows, ws, stream) : norm_bwd<1, false>(a, max_rows, ws, stream);
 }
 
 }  // namespace cgtp
