@@ -36,9 +36,9 @@
 namespace cgtp {
 namespace {
 
-constexpr int kNormThreads = 256;
-constexpr int kNormWarps = kNormThreads / 32;
-constexpr int kNormRows = 8;  // rows per thread, held in registers
+constexpr int kNormThreads = 256;  // of the tiles
+constexpr int kNormRows = 8;       // rows per thread of the tiles, held in registers
+constexpr int kFusedMost = 512;    // threads of a fused block, at most
 
 // VEC columns of a row; the packed fp32 operations take two at a time.
 template <int VEC>
@@ -177,16 +177,18 @@ struct Columns {
 
 // ------------------------------------------------------------------- fused
 struct Slabs {
-  int lanes;   // threads across a slab's columns (a power of two, at most 32)
-  int groups;  // whole groups of a slab
-  int count;   // slabs
-  int blocks;  // blocks per sample and slab (a cluster)
+  int lanes;    // threads across a slab's columns (a power of two, at most 32)
+  int groups;   // whole groups of a slab
+  int count;    // slabs
+  int blocks;   // blocks per sample and slab (a cluster)
+  int threads;  // of a block
+  int rows;     // rows per thread, held in registers
 };
 constexpr int kSlabColumns = 128;
 
 // What the threads of a block share: column sums by warp, then by column or by group.
 struct FusedShared {
-  float red[2][kNormWarps][kSlabColumns];
+  float red[2][kFusedMost / 32][kSlabColumns];
   float col[2][kSlabColumns];
   float sum[2][kSlabColumns];    // by group: this block's
   float total[2][kSlabColumns];  // by group: the cluster's
@@ -204,7 +206,7 @@ __device__ __forceinline__ Place place_of(const NormArgs& a, const Slabs& f) {
   p.sample = blockIdx.x / f.blocks / f.count;
   p.lane = threadIdx.x & (f.lanes - 1);
   p.ty = threadIdx.x / f.lanes;
-  p.nty = kNormThreads / f.lanes;
+  p.nty = blockDim.x / f.lanes;
   p.groups = min(f.groups, a.groups - slab * f.groups);
   p.c0 = slab * f.groups * cpg;
   p.columns = p.groups * cpg;
@@ -234,9 +236,9 @@ __device__ __forceinline__ void sum_rows(Vec<VEC> v, const Place& p, int lanes, 
 __device__ __forceinline__ void sum_groups(const Place& p, int cpg, int blocks, const float (*red)[kSlabColumns],
                                            float* sum, float* total) {
   __syncthreads();
-  for (int g = threadIdx.x >> 5; g < p.groups; g += kNormWarps) {
+  for (int g = threadIdx.x >> 5; g < p.groups; g += blockDim.x >> 5) {
     float s = 0.f;
-    for (int e = threadIdx.x & 31; e < kNormWarps * cpg; e += 32) s += red[e / cpg][g * cpg + e % cpg];
+    for (int e = threadIdx.x & 31; e < (int)(blockDim.x >> 5) * cpg; e += 32) s += red[e / cpg][g * cpg + e % cpg];
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if ((threadIdx.x & 31) == 0) {
@@ -247,7 +249,7 @@ __device__ __forceinline__ void sum_groups(const Place& p, int cpg, int blocks, 
   if (blocks > 1) {
     __syncwarp();
     tc::cluster_sync();
-    for (int g = threadIdx.x; g < p.groups; g += kNormThreads) {
+    for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
       float s = 0.f;
       for (int k = 0; k < blocks; ++k) s += tc::peer_load(tc::peer_addr(tc::smem_addr(sum + g), k));
       total[g] = s;
@@ -256,25 +258,27 @@ __device__ __forceinline__ void sum_groups(const Place& p, int cpg, int blocks, 
   __syncthreads();
 }
 
-template <int VEC, bool SILU>
-__global__ void __launch_bounds__(kNormThreads) norm_fused_kernel(NormArgs a, Slabs f) {
+template <int VEC, bool SILU, int ROWS>
+__global__ void __launch_bounds__(kFusedMost) norm_fused_kernel(NormArgs a, Slabs f) {
   __shared__ FusedShared sh;
   const Place p = place_of<VEC>(a, f);
   const int cpg = a.channels / a.groups, g0 = p.c0 / cpg;
   if (p.rows == 0) {
     if (p.part == 0)
-      for (int g = threadIdx.x; g < p.groups; g += kNormThreads) {
+      for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
         a.mean[(long long)p.sample * a.groups + g0 + g] = 0.f;
         a.rstd[(long long)p.sample * a.groups + g0 + g] = 1.f / sqrtf(a.eps);
       }
     return;  // every block of the cluster
   }
-  const int step = p.nty * kNormRows;
+  const int step = p.nty * ROWS;
   const bool held = p.r1 - p.r0 <= step;
-  Vec<VEC> v[kNormRows];
+  Columns<VEC> c{};
+  if (p.on) c.load_params(a, p.col);
+  Vec<VEC> v[ROWS];
   auto read = [&](int base) {
 #pragma unroll
-    for (int i = 0; i < kNormRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       const int r = base + p.ty + i * p.nty;
       v[i] = Vec<VEC>{};
       if (p.on && r < p.r1) v[i] = load_vec<VEC>(a.x + r * a.x_stride + p.col);
@@ -288,13 +292,13 @@ __global__ void __launch_bounds__(kNormThreads) norm_fused_kernel(NormArgs a, Sl
     float n = 0.f;
     Vec<VEC> s{}, d{};
 #pragma unroll
-    for (int i = 0; i < kNormRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       n += base + p.ty + i * p.nty < p.r1 ? 1.f : 0.f;
       s = s + v[i];  // rows that are not there are zero
     }
     const Vec<VEC> m = s * all<VEC>(1.f / fmaxf(n, 1.f)), minus = m * all<VEC>(-1.f);
 #pragma unroll
-    for (int i = 0; i < kNormRows; ++i)
+    for (int i = 0; i < ROWS; ++i)
       if (base + p.ty + i * p.nty < p.r1) {
         const Vec<VEC> q = v[i] + minus;
         d = fma(q, q, d);
@@ -310,26 +314,24 @@ __global__ void __launch_bounds__(kNormThreads) norm_fused_kernel(NormArgs a, Sl
   const float all_values = float(p.rows) * float(cpg);
   sum_rows<VEC>(mean * all<VEC>(p.on ? count : 0.f), p, f.lanes, sh.red[0]);
   sum_groups(p, cpg, f.blocks, sh.red[0], sh.sum[0], sh.total[0]);
-  Columns<VEC> c;
 #pragma unroll
   for (int j = 0; j < VEC; ++j) c.minus_mean.v[j] = p.on ? -(sh.total[0][(p.lane * VEC + j) / cpg] / all_values) : 0.f;
   const Vec<VEC> q = mean + c.minus_mean;
   sum_rows<VEC>(fma(q * q, all<VEC>(p.on ? count : 0.f), dev), p, f.lanes, sh.red[1]);
   sum_groups(p, cpg, f.blocks, sh.red[1], sh.sum[1], sh.total[1]);
   if (p.part == 0)
-    for (int g = threadIdx.x; g < p.groups; g += kNormThreads) {
+    for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
       const long long k = (long long)p.sample * a.groups + g0 + g;
       a.mean[k] = sh.total[0][g] / all_values;
       a.rstd[k] = 1.f / sqrtf(sh.total[1][g] / all_values + a.eps);
     }
   if (p.on) {
-    c.load_params(a, p.col);
 #pragma unroll
     for (int j = 0; j < VEC; ++j) c.rstd.v[j] = 1.f / sqrtf(sh.total[1][(p.lane * VEC + j) / cpg] / all_values + a.eps);
     for (int base = p.r0; base < p.r1; base += step) {
       if (!held) read(base);
 #pragma unroll
-      for (int i = 0; i < kNormRows; ++i) {
+      for (int i = 0; i < ROWS; ++i) {
         const int r = base + p.ty + i * p.nty;
         if (r < p.r1)
           store_vec<VEC>(a.y + r * a.y_stride + p.col, activate<SILU>(fma(c.gamma, c.normalised(v[i]), c.beta)));
@@ -343,28 +345,28 @@ __global__ void __launch_bounds__(kNormThreads) norm_fused_kernel(NormArgs a, Sl
 }
 
 // slots [sample * blocks + part][channel]: (sum gz, sum gz h) of the block's rows
-template <int VEC, bool SILU>
-__global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_fused_kernel(NormArgs a, Slabs f, float2* __restrict__ slots) {
+template <int VEC, bool SILU, int ROWS>
+__global__ void __launch_bounds__(kFusedMost) norm_bwd_fused_kernel(NormArgs a, Slabs f, float2* __restrict__ slots) {
   grid_dependents_launch();
   __shared__ FusedShared sh;
   const Place p = place_of<VEC>(a, f);
   const int cpg = a.channels / a.groups;
   float2* slot = slots + ((long long)p.sample * f.blocks + p.part) * a.channels + p.c0;
   if (p.rows == 0) {
-    for (int k = threadIdx.x; k < p.columns; k += kNormThreads) slot[k] = make_float2(0.f, 0.f);
+    for (int k = threadIdx.x; k < p.columns; k += blockDim.x) slot[k] = make_float2(0.f, 0.f);
     return;  // every block of the cluster
   }
-  const int step = p.nty * kNormRows;
+  const int step = p.nty * ROWS;
   const bool held = p.r1 - p.r0 <= step;
   Columns<VEC> c{};
   if (p.on) {
     c.load_params(a, p.col);
     c.load_stats(a, p.col, p.sample);
   }
-  Vec<VEC> h[kNormRows], gz[kNormRows];
+  Vec<VEC> h[ROWS], gz[ROWS];
   auto read = [&](int base) {
 #pragma unroll
-    for (int i = 0; i < kNormRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       const int r = base + p.ty + i * p.nty;
       h[i] = Vec<VEC>{};
       gz[i] = Vec<VEC>{};
@@ -374,7 +376,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_fused_kernel(NormArg
       }
     }
 #pragma unroll
-    for (int i = 0; i < kNormRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       if (base + p.ty + i * p.nty < p.r1) {
         h[i] = c.normalised(h[i]);
         gz[i] = activate_grad<SILU>(fma(c.gamma, h[i], c.beta), gz[i]);
@@ -385,7 +387,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_fused_kernel(NormArg
   for (int base = p.r0; base < p.r1; base += step) {
     read(base);
 #pragma unroll
-    for (int i = 0; i < kNormRows; ++i) {
+    for (int i = 0; i < ROWS; ++i) {
       s1 = s1 + gz[i];
       s2 = fma(gz[i], h[i], s2);
     }
@@ -393,10 +395,9 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_fused_kernel(NormArg
   sum_rows<VEC>(s1, p, f.lanes, sh.red[0]);
   sum_rows<VEC>(s2, p, f.lanes, sh.red[1]);
   __syncthreads();
-  for (int k = threadIdx.x; k < p.columns; k += kNormThreads) {
+  for (int k = threadIdx.x; k < p.columns; k += blockDim.x) {
     float x = 0.f, y = 0.f;
-#pragma unroll
-    for (int w = 0; w < kNormWarps; ++w) {
+    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
       x += sh.red[0][w][k];
       y += sh.red[1][w][k];
     }
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_fused_kernel(NormArg
   }
   __syncthreads();
   if (a.grad_x == nullptr) return;  // every block
-  for (int g = threadIdx.x >> 5; g < p.groups; g += kNormWarps) {
+  for (int g = threadIdx.x >> 5; g < p.groups; g += blockDim.x >> 5) {
     float x = 0.f, y = 0.f;
     for (int e = threadIdx.x & 31; e < cpg; e += 32) {
       x += sh.col[0][g * cpg + e];
@@ -426,7 +427,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_fused_kernel(NormArg
   if (f.blocks > 1) {
     __syncwarp();
     tc::cluster_sync();
-    for (int g = threadIdx.x; g < 2 * p.groups; g += kNormThreads) {
+    for (int g = threadIdx.x; g < 2 * p.groups; g += blockDim.x) {
       const int q = g >= p.groups, i = g - q * p.groups;
       float s = 0.f;
       for (int k = 0; k < f.blocks; ++k) s += tc::peer_load(tc::peer_addr(tc::smem_addr(&sh.sum[q][i]), k));
@@ -445,7 +446,7 @@ __global__ void __launch_bounds__(kNormThreads, 2) norm_bwd_fused_kernel(NormArg
     for (int base = p.r0; base < p.r1; base += step) {
       if (!held) read(base);
 #pragma unroll
-      for (int i = 0; i < kNormRows; ++i) {
+      for (int i = 0; i < ROWS; ++i) {
         const int r = base + p.ty + i * p.nty;
         if (r < p.r1)
           store_vec<VEC>(a.grad_x + r * a.gx_stride + p.col, c.rstd * fma(h[i], m2, fma(c.gamma, gz[i], m1)));
@@ -596,11 +597,12 @@ __device__ __forceinline__ float item_sum(float v, float* red) {
 // 2: TPI threads per (sample, group) join the slots.  Forward: the mean of all
 // values, then the squared deviations from it (each part's own plus its
 // mean's); backward: the group's means of t and t h.
+constexpr int kJoinThreads = 1024;
 template <int TPI, bool BWD>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(TPI > 32 ? TPI : kNormThreads)
     norm_join_kernel(NormArgs a, int rows_per_tile, const float2* __restrict__ slots, float2* __restrict__ terms) {
-  __shared__ float red[kNormThreads / 32];
-  const long long item = ((long long)blockIdx.x * kNormThreads + threadIdx.x) / TPI;
+  __shared__ float red[kJoinThreads / 32];
+  const long long item = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / TPI;
   if (item >= (long long)a.samples * a.groups) return;  // whole items leave together
   const int s = (int)(item / a.groups), g = (int)(item % a.groups), cpg = a.channels / a.groups;
   const int2 b = sample_rows(a, s);
@@ -611,6 +613,7 @@ __global__ void __launch_bounds__(kNormThreads)
   const int tid = threadIdx.x % TPI;
   auto rows_of = [&](int t) { return min(b.y, (t + 1) * rows_per_tile) - max(b.x, t * rows_per_tile); };
   float s1 = 0.f, s2 = 0.f;
+#pragma unroll 8
   for (long long q = tid; q < entries; q += TPI) {
     const int k = (int)(q / cpg), c = (int)(q % cpg);
     const float2 v = base[(long long)k * a.channels + c];
@@ -628,6 +631,7 @@ __global__ void __launch_bounds__(kNormThreads)
     s2 = item_sum<TPI>(s2, red);
     if (tid == 0) terms[item] = make_float2(mean, entries > 0 ? s2 / count : 0.f);
   } else {
+#pragma unroll 8
     for (long long q = tid; q < entries; q += TPI) {
       const int k = (int)(q / cpg), c = (int)(q % cpg);
       const float2 v = base[(long long)k * a.channels + c];
@@ -813,43 +817,59 @@ int rows_per_tile(int channels, int vec) { return kNormRows * (kNormThreads / la
 long long tiles_of(int n, int rows) { return ((long long)n + rows - 1) / rows; }
 bool vec4_rows(const void* p, long long stride) { return stride % 4 == 0 && ((uintptr_t)p & 15u) == 0; }
 
-// The fused split for these sizes, or count = 0 for the tiles.  The longest
-// sample is the caller's bound, else four times the average is expected.
-// Slabs are as wide as still lets the registers hold such a sample and gives
-// every SM a block, down to one 32-byte sector a row; then the rows are cut over a
-// cluster, as long as that leaves a block some rows to work on.
+// The fused split for these sizes, or count = 0 for the tiles.  Measured on
+// fp32 rows with SiLU, forward / backward in microseconds:
+//   256 samples x 30 rows x 128 channels: whole rows, 256 threads, 4 rows each 8.5 / 10.4
+//     (tiles 25 / 33);
+//   61 samples, 131 101 rows x 256: 64-byte slabs 87 / 135, 32-byte ones 142 / 174 (tiles 108 / 187);
+//   2 000 samples, 130 000 rows x 256: whole rows 98 / 139, 64-byte slabs over 200 (tiles 160 / 255);
+//   1 sample of 20 000 rows x 128: 64-byte slabs, 8 blocks of 512 threads 16.6 / 23 (tiles 18.7 / 32);
+//   1 sample of 130 000 rows x 256: that split 106 / 163, the tiles 93 / 157.
+// So slabs narrow, down to 64 bytes a row, while the usual sample does not fit
+// the registers and there are not yet many blocks; then few blocks become a
+// cluster of larger ones; and a longest sample that would keep its blocks
+// reading long after the others goes to the tiles.
 constexpr long long kFewBlocks = 148, kManyBlocks = 8 * kFewBlocks;
 template <int VEC>
-Slabs fused_slabs(const NormArgs& a, int max_rows) {
+Slabs fused_slabs(const NormArgs& a, int max_rows, bool backward) {
   Slabs f{};
   const int cpg = a.channels / a.groups;
   const int most = VEC == 4 ? kSlabColumns : 32;  // 32 lanes across
-  if (a.n == 0 || cpg > most) return f;
+  if (a.n == 0 || a.samples == 0 || cpg > most) return f;
   // slabs start on a vector: their groups are a multiple of this
   int unit = 1;
   while (unit * cpg % VEC != 0) ++unit;
   if (unit * cpg > most) return f;
-  long long rows = max_rows > 0 && max_rows < a.n ? max_rows : a.n;
-  if (max_rows <= 0 && a.samples > 1) {
-    const long long expected = 4LL * a.n / a.samples + 64;
-    if (expected < rows) rows = expected;
-  }
+  const long long average = ((long long)a.n + a.samples - 1) / a.samples;
+  // the longest sample: the caller's bound, else four times the average is expected
+  long long longest = max_rows > 0 ? max_rows : a.samples == 1 ? a.n : 4 * average + 64;
+  if (longest > a.n) longest = a.n;
+  const long long usual = longest < 2 * average ? longest : 2 * average;
   auto set = [&](int groups) {
     f.groups = groups < a.groups ? groups : a.groups;
     f.count = (a.groups + f.groups - 1) / f.groups;
     f.lanes = lanes_per_row(f.groups * cpg, VEC);
   };
-  auto held = [&]() { return (long long)kNormRows * (kNormThreads / f.lanes); };
+  auto held = [&]() { return (long long)f.rows * (f.threads / f.lanes); };
+  auto blocks = [&]() { return (long long)a.samples * f.count; };
+  f.threads = 256;
+  f.rows = 8;
   set(most / (unit * cpg) * unit);
-  while (f.groups > unit && f.groups * cpg > 8 && (held() < rows || (long long)a.samples * f.count < kFewBlocks)) {
+  while (f.groups > unit && f.groups * cpg > 16 && blocks() < kManyBlocks && (held() < usual || blocks() < kFewBlocks)) {
     const int half = (f.groups / unit + 1) / 2 * unit;
     if (half == f.groups) break;
     set(half);
   }
   f.blocks = 1;
-  while (f.blocks < 8 && held() * f.blocks < rows && (long long)a.samples * f.count * f.blocks * 2 <= kManyBlocks) f.blocks *= 2;
-  // a block that reads its rows again and again while others are done: leave that to the tiles
-  if (held() * f.blocks * 16 < rows || (long long)a.samples * f.count * f.blocks > 0x7fffffffLL) f.count = 0;
+  while (f.blocks < 8 && held() * f.blocks < longest && blocks() * f.blocks < kFewBlocks) f.blocks *= 2;
+  if (blocks() * f.blocks <= kFewBlocks && held() * f.blocks < longest) f.threads = kFusedMost;
+  if (f.blocks == 1) {
+    // small samples: fewer rows in registers, then fewer threads.  Many blocks: more of them a SM
+    // (the forward only: the backward would compute its rows twice as often)
+    if (held() / 2 >= usual || (!backward && blocks() >= kManyBlocks)) f.rows = 4;
+    while (f.threads > 128 && held() / 2 >= usual) f.threads /= 2;
+  }
+  if (held() * f.blocks * (blocks() < 4 * kFewBlocks ? 8 : 32) < longest || blocks() * f.blocks > 0x7fffffffLL) f.count = 0;
   return f;
 }
 
@@ -857,7 +877,7 @@ template <class... P, class... A>
 cudaError_t launch_cluster(void (*kernel)(P...), const NormArgs& a, const Slabs& f, cudaStream_t stream, A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)((long long)a.samples * f.count * f.blocks));
-  cfg.blockDim = dim3(kNormThreads);
+  cfg.blockDim = dim3(f.threads);
   cfg.stream = stream;
   cudaLaunchAttribute attr{};
   attr.id = cudaLaunchAttributeClusterDimension;
@@ -876,15 +896,17 @@ cudaError_t join(const NormArgs& a, int rows, const float2* slots, float2* terms
   const bool wide = ((double)a.n / a.samples / rows + 1) * (a.channels / a.groups) > 512;
   const long long blocks = wide ? items : (items * 32 + kNormThreads - 1) / kNormThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if (wide) norm_join_kernel<kNormThreads, BWD><<<(unsigned)blocks, kNormThreads, 0, stream>>>(a, rows, slots, terms);
+  if (wide) norm_join_kernel<kJoinThreads, BWD><<<(unsigned)blocks, kJoinThreads, 0, stream>>>(a, rows, slots, terms);
   else norm_join_kernel<32, BWD><<<(unsigned)blocks, kNormThreads, 0, stream>>>(a, rows, slots, terms);
   return cudaGetLastError();
 }
 
 template <int VEC, bool SILU>
 cudaError_t norm_fwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t stream) {
-  const Slabs f = fused_slabs<VEC>(a, max_rows);
-  if (f.count > 0) return launch_cluster(norm_fused_kernel<VEC, SILU>, a, f, stream);
+  const Slabs f = fused_slabs<VEC>(a, max_rows, false);
+  if (f.count > 0)
+    return f.rows == 4 ? launch_cluster(norm_fused_kernel<VEC, SILU, 4>, a, f, stream)
+                       : launch_cluster(norm_fused_kernel<VEC, SILU, 8>, a, f, stream);
   const int lpr = lanes_per_row(a.channels, VEC), rows = rows_per_tile(a.channels, VEC);
   const dim3 grid((unsigned)tiles_of(a.n, rows), (unsigned)((a.channels + lpr * VEC - 1) / (lpr * VEC)));
   cudaError_t e = cudaSuccess;
@@ -909,9 +931,10 @@ cudaError_t norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t str
   float2* terms = (float2*)ws;
   float2* sums = (float2*)((char*)ws + terms_bytes(a));
   float2* slots = (float2*)((char*)ws + terms_bytes(a) + sums_bytes(a));
-  const Slabs f = fused_slabs<VEC>(a, max_rows);
-  if (f.count > 0 && a.samples > 0) {
-    const cudaError_t e = launch_cluster(norm_bwd_fused_kernel<VEC, SILU>, a, f, stream, slots);
+  const Slabs f = fused_slabs<VEC>(a, max_rows, true);
+  if (f.count > 0) {
+    const cudaError_t e = f.rows == 4 ? launch_cluster(norm_bwd_fused_kernel<VEC, SILU, 4>, a, f, stream, slots)
+                                      : launch_cluster(norm_bwd_fused_kernel<VEC, SILU, 8>, a, f, stream, slots);
     return e != cudaSuccess ? e : sum_params(a, (long long)a.samples * f.blocks, slots, sums, stream);
   }
   const int lpr = lanes_per_row(a.channels, VEC), rows = rows_per_tile(a.channels, VEC);
