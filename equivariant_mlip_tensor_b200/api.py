@@ -6,6 +6,8 @@ contiguous, fp32 (features, weights, vectors) or int32 (indices), in the
 layouts of include/cgtp.h.
 """
 import ctypes
+import functools
+import math
 from dataclasses import dataclass
 from typing import Optional
 
@@ -159,10 +161,16 @@ def scatter_add_rows(idx, src, dst):
 
 # ------------------------------------------------------------ training-side operators
 # These run on the device of their tensors, on that device's current stream.
-def _same_device(first, **others):
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+# At the sizes of a small batch the call itself is what they cost, so it is kept
+# short: plain addresses, sizes asked for once per shape.
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(dev, *named):
+    for name, t in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
 
 
 def _check_rows(t, name, n=None, width=None):
@@ -172,12 +180,15 @@ def _check_rows(t, name, n=None, width=None):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype != torch.float32:
         raise ValueError(f"{name} must be {torch.float32}, got {t.dtype}")
-    if t.dim() != 2 or (n is not None and t.shape[0] != n) or (width is not None and t.shape[1] != width):
+    shape = t.shape
+    if len(shape) != 2 or (n is not None and shape[0] != n) or (width is not None and shape[1] != width):
         raise ValueError(f"{name} must be [{'n' if n is None else n}][{'width' if width is None else width}], "
-                         f"got {tuple(t.shape)}")
-    n, width = t.shape
-    stride = t.stride(0) if n > 1 else max(width, t.stride(0))
-    if (width > 1 and t.stride(1) != 1) or stride < width:
+                         f"got {tuple(shape)}")
+    n, width = shape
+    stride, step = t.stride()
+    if n <= 1:
+        stride = max(width, stride)
+    if (width > 1 and step != 1) or stride < width:
         raise ValueError(f"{name} must have contiguous rows that do not overlap, got strides {t.stride()}")
     return stride
 
@@ -188,9 +199,17 @@ def _check_vector(t, dtype, name, size):
         raise ValueError(f"{name} must have {size} elements, got {tuple(t.shape)}")
 
 
+def _current_stream(index):
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same number without a stream object around it, where this torch has the short way (2 us a call)
+_current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
 def _call_on(dev, name, *args):
     """Call an entry point on the tensors' device and that device's current stream."""
-    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    stream = _current_stream(dev.index)
     if dev.index == torch.cuda.current_device():
         call(name, *args, stream)
     else:
@@ -201,12 +220,13 @@ def _call_on(dev, name, *args):
 def _workspace(workspace, need, dev):
     """(tensor, bytes): the caller's workspace, or one of the size asked for."""
     if workspace is None:
-        return torch.empty(max(need, 256), dtype=torch.uint8, device=dev), need
+        return (torch.empty(need, dtype=torch.uint8, device=dev) if need else None), need
     if not workspace.is_cuda or not workspace.is_contiguous() or workspace.device != dev:
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     return workspace, workspace.numel() * workspace.element_size()
 
 
+@functools.lru_cache(maxsize=256)
 def _bytes(name, *args):
     b = ctypes.c_size_t()
     call(name, *args, ctypes.byref(b))
@@ -229,9 +249,10 @@ def token_sort(tokens, n_rows, workspace=None):
     """Stable sort of tokens [n] into [0, n_rows) for embed_backward."""
     _check(tokens, torch.int32, "tokens")
     n, dev = tokens.numel(), tokens.device
-    order, srt = torch.empty((2, n), dtype=torch.int32, device=dev)
+    order = torch.empty(n, dtype=torch.int32, device=dev)
+    srt = torch.empty(n, dtype=torch.int32, device=dev)
     ws, nb = _workspace(workspace, token_sort_workspace_bytes(n, n_rows), dev)
-    _call_on(dev, "cgtp_token_sort", n, n_rows, _ptr(tokens), _ptr(order), _ptr(srt), _ptr(ws), nb)
+    _call_on(dev, "cgtp_token_sort", n, n_rows, _at(tokens), _at(order), _at(srt), _at(ws), nb)
     return TokenOrder(n_rows, order, srt)
 
 
@@ -243,12 +264,12 @@ def embed_forward(tokens, table, scale=1.0, out=None):
     _check(table, torch.float32, "table")
     if table.dim() != 2:
         raise ValueError(f"table must be [n_rows][width], got {tuple(table.shape)}")
-    n, (n_rows, width) = tokens.numel(), table.shape
+    n, (n_rows, width), dev = tokens.numel(), table.shape, table.device
     if out is None:
-        out = torch.empty((n, width), dtype=torch.float32, device=table.device)
+        out = torch.empty((n, width), dtype=torch.float32, device=dev)
     stride = _check_rows(out, "out", n, width)
-    _same_device(table, tokens=tokens, out=out)
-    _call_on(table.device, "cgtp_embed_forward", n, n_rows, width, _ptr(tokens), _ptr(table), float(scale), _ptr(out), stride)
+    _same_device(dev, ("tokens", tokens), ("out", out))
+    _call_on(dev, "cgtp_embed_forward", n, n_rows, width, _at(tokens), _at(table), scale, _at(out), stride)
     return out
 
 
@@ -266,13 +287,14 @@ def embed_backward(order, grad_out, scale=1.0, out=None, workspace=None):
     width, dev = grad_out.shape[1], grad_out.device
     if out is None:
         out = torch.empty((order.n_rows, width), dtype=torch.float32, device=dev)
-    _check(out, torch.float32, "out")
-    if tuple(out.shape) != (order.n_rows, width):
-        raise ValueError(f"out must be [{order.n_rows}][{width}], got {tuple(out.shape)}")
-    _same_device(grad_out, order=order.order, sorted=order.sorted, out=out)
+    else:
+        _check(out, torch.float32, "out")
+        if tuple(out.shape) != (order.n_rows, width):
+            raise ValueError(f"out must be [{order.n_rows}][{width}], got {tuple(out.shape)}")
+    _same_device(dev, ("order", order.order), ("sorted", order.sorted), ("out", out))
     ws, nb = _workspace(workspace, embed_backward_workspace_bytes(n, width), dev)
-    _call_on(dev, "cgtp_embed_backward", n, order.n_rows, width, _ptr(order.order), _ptr(order.sorted), _ptr(grad_out),
-             stride, float(scale), _ptr(out), _ptr(ws), nb)
+    _call_on(dev, "cgtp_embed_backward", n, order.n_rows, width, _at(order.order), _at(order.sorted), _at(grad_out),
+             stride, scale, _at(out), _at(ws), nb)
     return out
 
 
@@ -312,11 +334,12 @@ def group_norm_forward(x, gamma, beta, groups, graph_ptr=None, eps=1e-5, activat
     if out is None:
         out = torch.empty((n, c), dtype=torch.float32, device=dev)
     out_stride = _check_rows(out, "out", n, c)
-    _same_device(x, gamma=gamma, beta=beta, graph_ptr=graph_ptr, out=out)
-    mean, rstd = torch.empty((2, b, groups), dtype=torch.float32, device=dev)
+    _same_device(dev, ("gamma", gamma), ("beta", beta), ("graph_ptr", graph_ptr), ("out", out))
+    mean = torch.empty((b, groups), dtype=torch.float32, device=dev)
+    rstd = torch.empty((b, groups), dtype=torch.float32, device=dev)
     ws, nb = _workspace(workspace, group_norm_workspace_bytes(n, b, c, groups), dev)
-    _call_on(dev, "cgtp_group_norm_forward", n, b, c, groups, _ptr(graph_ptr), max_rows, _ptr(x), stride, _ptr(gamma),
-             _ptr(beta), float(eps), ACTIVATIONS[activation], _ptr(out), out_stride, _ptr(mean), _ptr(rstd), _ptr(ws), nb)
+    _call_on(dev, "cgtp_group_norm_forward", n, b, c, groups, _at(graph_ptr), max_rows, _at(x), stride, _at(gamma),
+             _at(beta), eps, ACTIVATIONS[activation], _at(out), out_stride, _at(mean), _at(rstd), _at(ws), nb)
     return out, mean, rstd
 
 
@@ -333,18 +356,22 @@ def group_norm_backward(x, gamma, beta, groups, mean, rstd, grad_y, graph_ptr=No
         if t.numel() != b * groups:
             raise ValueError(f"{nm} must be [{b}][{groups}], got {tuple(t.shape)}")
     gx_stride = 0
-    if want_x:
+    if not want_x:
+        grad_x = None
+    else:
         if grad_x is None:
             grad_x = torch.empty((n, c), dtype=torch.float32, device=dev)
         gx_stride = _check_rows(grad_x, "grad_x", n, c)
-    else:
-        grad_x = None
-    _same_device(x, gamma=gamma, beta=beta, graph_ptr=graph_ptr, mean=mean, rstd=rstd, grad_y=grad_y, grad_x=grad_x)
-    gg, gb = torch.empty((2, c), dtype=torch.float32, device=dev) if want_params else (None, None)
+    _same_device(dev, ("gamma", gamma), ("beta", beta), ("graph_ptr", graph_ptr), ("mean", mean), ("rstd", rstd),
+                 ("grad_y", grad_y), ("grad_x", grad_x))
+    gg = gb = None
+    if want_params:
+        gg = torch.empty(c, dtype=torch.float32, device=dev)
+        gb = torch.empty(c, dtype=torch.float32, device=dev)
     ws, nb = _workspace(workspace, group_norm_workspace_bytes(n, b, c, groups), dev)
-    _call_on(dev, "cgtp_group_norm_backward", n, b, c, groups, _ptr(graph_ptr), max_rows, _ptr(x), stride, _ptr(gamma),
-             _ptr(beta), _ptr(mean), _ptr(rstd), ACTIVATIONS[activation], _ptr(grad_y), gy_stride, _ptr(grad_x), gx_stride,
-             _ptr(gg), _ptr(gb), _ptr(ws), nb)
+    _call_on(dev, "cgtp_group_norm_backward", n, b, c, groups, _at(graph_ptr), max_rows, _at(x), stride, _at(gamma),
+             _at(beta), _at(mean), _at(rstd), ACTIVATIONS[activation], _at(grad_y), gy_stride, _at(grad_x), gx_stride,
+             _at(gg), _at(gb), _at(ws), nb)
     return grad_x, gg, gb
 
 
@@ -356,19 +383,20 @@ def orthogonalise(update, steps=5, scale=1.0, out=None, workspace=None):
     """scale * (near-)orthogonal factor of each matrix of update [..., rows, cols]
     by Newton-Schulz products (cgtp_orthogonalise); out may be update."""
     _check(update, torch.float32, "update")
-    if update.dim() < 2:
-        raise ValueError(f"update must be [..., rows, cols], got {tuple(update.shape)}")
-    rows, cols = update.shape[-2:]
-    batch = int(np.prod(update.shape[:-2]))
+    shape = update.shape
+    if len(shape) < 2:
+        raise ValueError(f"update must be [..., rows, cols], got {tuple(shape)}")
+    rows, cols = shape[-2:]
+    batch, dev = math.prod(shape[:-2]), update.device
     if out is None:
         out = torch.empty_like(update)
-    _check(out, torch.float32, "out")
-    if out.shape != update.shape:
-        raise ValueError(f"out must have the shape of update, got {tuple(out.shape)}")
-    _same_device(update, out=out)
-    ws, nb = _workspace(workspace, orthogonalise_workspace_bytes(batch, rows, cols), update.device)
-    _call_on(update.device, "cgtp_orthogonalise", batch, rows, cols, steps, float(scale), _ptr(update), _ptr(out), _ptr(ws),
-             nb)
+    else:
+        _check(out, torch.float32, "out")
+        if out.shape != shape:
+            raise ValueError(f"out must have the shape of update, got {tuple(out.shape)}")
+        _same_device(dev, ("out", out))
+    ws, nb = _workspace(workspace, orthogonalise_workspace_bytes(batch, rows, cols), dev)
+    _call_on(dev, "cgtp_orthogonalise", batch, rows, cols, steps, scale, _at(update), _at(out), _at(ws), nb)
     return out
 
 

@@ -17,6 +17,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "common.cuh"
 #include "train_ops.h"
 
 namespace cgtp {
@@ -25,28 +26,143 @@ namespace {
 // ------------------------------------------------------------------ sort
 // Least-significant-digit radix sort of (key, position), 8 bits a pass, where
 // the key of a token outside [0, n_rows) is n_rows (so those come last).
-// Every pass is two steps over tiles of kSortTile tokens: the digit counts
-// of each tile, then the scatter, in which each tile adds up the counts of the
-// tiles before it (and of smaller digits) itself.  The scatter of one pass
-// counts the next pass's digits as it places them (integer atomics: the
-// counts do not depend on their order), so a sort of p passes is p + 1
-// launches.  Beyond kSortScanTiles tiles that sum over tiles, which every tile
-// repeats, would grow with their square: one more launch a pass then turns
-// the counts into prefixes first.  A warp ranks equal digits by ballot of
-// matching lanes in position order, which keeps the sort stable.
+// Every warp ranks a stretch of consecutive tokens: lanes with equal digits find
+// one another by a ballot per bit, in position order, which keeps the sort
+// stable.
+//
+// Up to kBlockTokens tokens: one block, all passes in shared memory (7 680
+// tokens of 16 species 8.8 -> FIXME us).  Beyond: tiles of kSortTile tokens.  The
+// first launch counts each tile's digits; each pass is one more, in which every
+// tile adds up the counts of the tiles before it (and of smaller digits)
+// itself, places its tokens, and counts the next pass's digits as it does
+// (integer atomics: the counts do not depend on their order).  Beyond
+// kSortScanTiles tiles that sum over tiles, which every tile repeats, would
+// grow with their square: one more launch a pass then turns the counts into
+// prefixes first.
 constexpr int kSortThreads = 512;
-constexpr int kSortItems = 8;
+constexpr int kSortItems = 4;
 constexpr int kSortTile = kSortThreads * kSortItems;  // tokens per tile
-constexpr int kSortWarps = kSortThreads / 32;
 constexpr int kDigits = 256;
-constexpr int kSortScanTiles = 256;
+constexpr int kSortScanTiles = 512;
+constexpr int kBlockThreads = 1024;
+constexpr int kBlockItems = 8;
+constexpr int kBlockTokens = kBlockThreads * kBlockItems;
 
 __device__ __forceinline__ int token_key(int t, int n_rows) { return (unsigned)t < (unsigned)n_rows ? t : n_rows; }
 
-__global__ void __launch_bounds__(kSortThreads) sort_count_kernel(int n, int n_rows, const int* __restrict__ tokens,
-                                                                   int* __restrict__ counts) {
+// Ranks of a warp's ITEMS x 32 keys (key < 0: none) among its equal digits, in
+// position order; count [digit], zero before, receives the warp's counts.
+template <int ITEMS>
+__device__ __forceinline__ void rank_digits(const int (&key)[ITEMS], int shift, int* count, int (&rank)[ITEMS]) {
+  const int lane = threadIdx.x & 31;
+  unsigned same[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int d = key[i] >> shift;
+    same[i] = __ballot_sync(0xffffffffu, key[i] >= 0);
+#pragma unroll
+    for (int b = 0; b < 8; ++b) {
+      const bool set = (d >> b) & 1;
+      const unsigned m = __ballot_sync(0xffffffffu, set);
+      same[i] &= set ? m : ~m;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    const int d = (key[i] >> shift) & (kDigits - 1), lower = __popc(same[i] & ((1u << lane) - 1u));
+    int seen = 0;
+    if (key[i] >= 0) seen = count[d];
+    __syncwarp();
+    if (key[i] >= 0 && lower == 0) count[d] = seen + __popc(same[i]);
+    __syncwarp();
+    rank[i] = seen + lower;
+  }
+}
+// Exclusive prefix of v over threads 0..255 (every thread of the block calls).
+__device__ __forceinline__ int prefix_digits(int v, int* warp_sums) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31 && w < kDigits / 32) warp_sums[w] = incl;
+  __syncthreads();
+  int base = 0;
+#pragma unroll
+  for (int q = 0; q < kDigits / 32; ++q)
+    if (q < w) base += warp_sums[q];
+  return base + incl - v;
+}
+
+template <int ITEMS>
+__global__ void __launch_bounds__(kBlockThreads)
+    sort_block_kernel(int n, int n_rows, int passes, const int* __restrict__ tokens, int* __restrict__ order,
+                      int* __restrict__ sorted) {
+  extern __shared__ int block_smem[];
+  int* keys = block_smem;
+  int* places = keys + kBlockThreads * ITEMS;
+  int(*count)[kDigits] = (int(*)[kDigits])(places + kBlockThreads * ITEMS);  // [warp][digit]
+  __shared__ int warp_sums[kDigits / 32];
+  const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5, base = w * 32 * ITEMS, warps = (n + 32 * ITEMS - 1) / (32 * ITEMS);
+  int key[ITEMS], pos[ITEMS], rank[ITEMS];
+#pragma unroll
+  for (int i = 0; i < ITEMS; ++i) {
+    pos[i] = base + 32 * i + lane;
+    key[i] = pos[i] < n ? token_key(tokens[pos[i]], n_rows) : -1;
+  }
+  for (int p = 0; p < passes; ++p) {
+    const int shift = 8 * p;
+    for (int d = lane; d < kDigits; d += 32) count[w][d] = 0;
+    __syncwarp();
+    rank_digits(key, shift, count[w], rank);
+    __syncthreads();
+    int total = 0;
+    if (tid < kDigits)
+#pragma unroll 8
+      for (int q = 0; q < warps; ++q) total += count[q][tid];
+    int run = prefix_digits(total, warp_sums);
+    if (tid < kDigits)
+#pragma unroll 8
+      for (int q = 0; q < warps; ++q) {
+        const int c = count[q][tid];
+        count[q][tid] = run;
+        run += c;
+      }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ITEMS; ++i)
+      if (key[i] >= 0) {
+        const int to = count[w][(key[i] >> shift) & (kDigits - 1)] + rank[i];
+        keys[to] = key[i];
+        places[to] = pos[i];
+      }
+    __syncthreads();
+    if (p + 1 < passes) {
+#pragma unroll
+      for (int i = 0; i < ITEMS; ++i) {
+        const int k = base + 32 * i + lane;
+        if (k < n) {
+          key[i] = keys[k];
+          pos[i] = places[k];
+        }
+      }
+    }
+  }
+  for (int k = tid; k < n; k += kBlockThreads) {
+    sorted[k] = keys[k];
+    order[k] = places[k];
+  }
+}
+
+// counts: [pass][tile][digit], the passes behind the first cleared here.
+__global__ void __launch_bounds__(kSortThreads)
+    sort_count_kernel(int n, int n_rows, int passes, long long per_pass, const int* __restrict__ tokens,
+                      int* __restrict__ counts) {
+  grid_dependents_launch();
   __shared__ int c[kDigits];
-  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) c[d] = 0;
+  if (threadIdx.x < kDigits) c[threadIdx.x] = 0;
   __syncthreads();
   const long long base = (long long)blockIdx.x * kSortTile;
 #pragma unroll
@@ -55,13 +171,17 @@ __global__ void __launch_bounds__(kSortThreads) sort_count_kernel(int n, int n_r
     if (k < n) atomicAdd(&c[token_key(tokens[k], n_rows) & (kDigits - 1)], 1);
   }
   __syncthreads();
-  for (int d = threadIdx.x; d < kDigits; d += kSortThreads) counts[(long long)blockIdx.x * kDigits + d] = c[d];
+  if (threadIdx.x < kDigits)
+    for (int p = 0; p < passes; ++p)
+      counts[p * per_pass + (long long)blockIdx.x * kDigits + threadIdx.x] = p == 0 ? c[threadIdx.x] : 0;
 }
 
 // One block per digit: the counts of its digit become the sums over earlier
 // tiles, and their total goes behind the last tile's counts.
 __global__ void __launch_bounds__(kSortThreads) sort_prefix_kernel(int tiles, int* __restrict__ counts) {
-  __shared__ int warp_sums[kSortWarps];
+  grid_dependents_launch();
+  grid_dependency_wait();
+  __shared__ int warp_sums[kSortThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   int carry = 0;
   for (int b0 = 0; b0 < tiles; b0 += kSortThreads) {
@@ -76,7 +196,7 @@ __global__ void __launch_bounds__(kSortThreads) sort_prefix_kernel(int tiles, in
     if (lane == 31) warp_sums[w] = incl;
     __syncthreads();
     int base = carry;
-    for (int q = 0; q < kSortWarps; ++q) {
+    for (int q = 0; q < kSortThreads / 32; ++q) {
       if (q < w) base += warp_sums[q];
       carry += warp_sums[q];
     }
@@ -86,47 +206,20 @@ __global__ void __launch_bounds__(kSortThreads) sort_prefix_kernel(int tiles, in
   if (tid == 0) counts[(long long)tiles * kDigits + blockIdx.x] = carry;
 }
 
-// One scatter pass over digit bits [shift, shift + 8).  keys_in = nullptr: the
-// first pass, keys from the tokens and positions 0..n-1.  next_counts
-// (nullable): the next pass's tile counts, zeroed before.
+// One pass over digit bits [shift, shift + 8).  keys_in = nullptr: the first
+// pass, keys from the tokens and positions 0..n-1.  next_counts (nullable): the
+// next pass's tile counts.
 __global__ void __launch_bounds__(kSortThreads)
     sort_scatter_kernel(int n, int n_rows, int shift, const int* __restrict__ tokens, const int* __restrict__ keys_in,
                         const int* __restrict__ pos_in, const int* __restrict__ counts, int* __restrict__ keys_out,
                         int* __restrict__ pos_out, int* __restrict__ next_counts) {
-  __shared__ int warp_count[kSortWarps][kDigits];
-  __shared__ int start[kDigits];
-  __shared__ int scan[kDigits / 32];
+  grid_dependents_launch();
+  __shared__ int count[kSortThreads / 32][kDigits];
+  __shared__ int part[2][2][kDigits];  // [half of the tiles][before, all][digit]
+  __shared__ int warp_sums[kDigits / 32];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
-  for (int d = tid; d < kSortWarps * kDigits; d += kSortThreads) (&warp_count[0][0])[d] = 0;
-  // start of each digit of this tile: smaller digits of every tile, then the same digit of earlier tiles
-  int before = 0, incl = 0, total = 0;
-  if (tid < kDigits) {
-    if (gridDim.x > kSortScanTiles) {  // prefixes already
-      before = counts[(long long)blockIdx.x * kDigits + tid];
-      total = counts[(long long)gridDim.x * kDigits + tid];
-    } else {
-#pragma unroll 8
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        const int c = counts[b * kDigits + tid];
-        if (b < (int)blockIdx.x) before += c;
-        total += c;
-      }
-    }
-    incl = total;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) scan[w] = incl;
-  }
-  __syncthreads();
-  if (tid < kDigits) {
-    int base = 0;
-    for (int q = 0; q < w; ++q) base += scan[q];
-    start[tid] = base + incl - total + before;
-  }
-  // ranks inside the warp's own stretch of kSortItems x 32 consecutive tokens
+  for (int d = lane; d < kDigits; d += 32) count[w][d] = 0;
+  grid_dependency_wait();
   int key[kSortItems], pos[kSortItems], rank[kSortItems];
   const long long base = (long long)blockIdx.x * kSortTile + w * (32 * kSortItems);
 #pragma unroll
@@ -139,26 +232,37 @@ __global__ void __launch_bounds__(kSortThreads)
       pos[i] = pos_in == nullptr ? (int)k : pos_in[k];
     }
   }
-  __syncthreads();
-#pragma unroll
-  for (int i = 0; i < kSortItems; ++i) {
-    const int d = key[i] < 0 ? kDigits : (key[i] >> shift) & (kDigits - 1);
-    const unsigned same = __match_any_sync(0xffffffffu, d);
-    const int lower = __popc(same & ((1u << lane) - 1u));
-    int seen = 0;
-    if (d < kDigits) seen = warp_count[w][d];
-    __syncwarp();
-    if (d < kDigits && lower == 0) warp_count[w][d] = seen + __popc(same);
-    __syncwarp();
-    rank[i] = seen + lower;
+  // start of each digit of this tile: smaller digits of every tile, then the
+  // same digit of earlier tiles; each half of the threads adds up half of the tiles
+  const int d = tid & (kDigits - 1), half = tid / kDigits, tiles = gridDim.x;
+  int before = 0, all = 0;
+  if (tiles > kSortScanTiles) {  // prefixes already
+    if (half == 0) {
+      before = counts[(long long)blockIdx.x * kDigits + d];
+      all = counts[(long long)tiles * kDigits + d];
+    }
+  } else {
+    const int b0 = half * tiles / 2, b1 = (half + 1) * tiles / 2;
+#pragma unroll 16
+    for (int b = b0; b < b1; ++b) {
+      const int c = counts[b * kDigits + d];
+      if (b < (int)blockIdx.x) before += c;
+      all += c;
+    }
   }
+  part[half][0][d] = before;
+  part[half][1][d] = all;
+  __syncwarp();
+  rank_digits(key, shift, count[w], rank);
   __syncthreads();
-  if (tid < kDigits) {  // the warps' counts become their starts
-    int run = start[tid];
+  all = half == 0 ? part[0][1][d] + part[1][1][d] : 0;
+  int run = prefix_digits(all, warp_sums);
+  if (half == 0) {  // the warps' counts become their starts
+    run += part[0][0][d] + part[1][0][d];
 #pragma unroll
-    for (int q = 0; q < kSortWarps; ++q) {
-      const int c = warp_count[q][tid];
-      warp_count[q][tid] = run;
+    for (int q = 0; q < kSortThreads / 32; ++q) {
+      const int c = count[q][d];
+      count[q][d] = run;
       run += c;
     }
   }
@@ -166,7 +270,7 @@ __global__ void __launch_bounds__(kSortThreads)
 #pragma unroll
   for (int i = 0; i < kSortItems; ++i) {
     if (key[i] < 0) continue;
-    const int to = warp_count[w][(key[i] >> shift) & (kDigits - 1)] + rank[i];
+    const int to = count[w][(key[i] >> shift) & (kDigits - 1)] + rank[i];
     keys_out[to] = key[i];
     pos_out[to] = pos[i];
     if (next_counts != nullptr)
@@ -221,17 +325,18 @@ struct EmbedBwdArgs {
 constexpr int kEmbedThreads = 256;
 constexpr int kEmbedUnroll = 8;
 
-// Blocks below chunk_blocks: one worker per (chunk, column slice).  The other
-// blocks write zeros into the rows that no token has, found by a search of
-// the sorted tokens; they run beside the first ones.
+// The first clear_blocks blocks write zeros into the rows that no token has,
+// found by a search of the sorted tokens; in the others, one worker takes one
+// (chunk, column slice).
 template <int VEC>
-__global__ void __launch_bounds__(kEmbedThreads) embed_bwd_kernel(EmbedBwdArgs a, int chunk_blocks) {
+__global__ void __launch_bounds__(kEmbedThreads) embed_bwd_kernel(EmbedBwdArgs a, int clear_blocks) {
+  grid_dependents_launch();
   const int lane = threadIdx.x & (a.lpr - 1);
-  if ((int)blockIdx.x >= chunk_blocks) {
-    const long long stride = (long long)(gridDim.x - chunk_blocks) * (kEmbedThreads / 32);
+  if ((int)blockIdx.x < clear_blocks) {
+    const long long stride = (long long)clear_blocks * (kEmbedThreads / 32);
     const int wl = threadIdx.x & 31;
-    for (long long r0 = ((long long)(blockIdx.x - chunk_blocks) * (kEmbedThreads / 32) + (threadIdx.x >> 5)) * 32;
-         r0 < a.n_rows; r0 += stride * 32) {
+    for (long long r0 = ((long long)blockIdx.x * (kEmbedThreads / 32) + (threadIdx.x >> 5)) * 32; r0 < a.n_rows;
+         r0 += stride * 32) {
       // each lane searches one of 32 rows, then the warp clears the empty ones together
       const int r = (int)(r0 + wl);
       bool empty = false;
@@ -252,7 +357,7 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_bwd_kernel(EmbedBwdArgs a
     }
     return;
   }
-  const long long worker = ((long long)blockIdx.x * kEmbedThreads + threadIdx.x) / a.lpr;
+  const long long worker = ((long long)(blockIdx.x - clear_blocks) * kEmbedThreads + threadIdx.x) / a.lpr;
   const int chunk = (int)(worker / a.slices), slice = (int)(worker % a.slices);
   const int col = (slice * a.lpr + lane) * VEC;
   if (chunk >= a.n_chunks || col >= a.width) return;
@@ -301,49 +406,73 @@ __global__ void __launch_bounds__(kEmbedThreads) embed_bwd_kernel(EmbedBwdArgs a
   else finish(run);
 }
 
-// Joins the runs that cross chunk borders: one block per (chunk in which such
-// a run starts, slice); the block's workers take the run's later chunks in
-// turn and their sums meet in shared memory in a fixed order.
+// Joins the runs that cross chunk borders.  A worker per chunk adds up a run
+// that starts there and ends within the next kShortRun chunks; the block's
+// workers take the longer ones together, one after the other, and their sums
+// meet in shared memory in a fixed order.
+constexpr int kShortRun = 4;
 template <int VEC>
 __global__ void __launch_bounds__(kEmbedThreads) embed_join_kernel(EmbedBwdArgs a) {
+  grid_dependency_wait();
   __shared__ Vec<VEC> part[kEmbedThreads];
-  const int chunk = blockIdx.x, p0 = chunk * a.chunk, p1 = p0 + a.chunk;
-  if (p1 >= a.n) return;
-  const int run = a.sorted[p1 - 1];
-  if (a.sorted[p1] != run || (unsigned)run >= (unsigned)a.n_rows) return;
-  if (p0 > 0 && a.sorted[p0 - 1] == run) return;  // it started earlier
-  int lo = p1, hi = a.n;  // first position behind the run
-  while (lo < hi) {
-    const int mid = lo + (hi - lo) / 2;
-    if (a.sorted[mid] <= run) lo = mid + 1;
-    else hi = mid;
-  }
-  const int last = (lo - 1) / a.chunk;
+  __shared__ int long_run[kEmbedThreads];  // by worker: the row of a long run, or -1
   const int lane = threadIdx.x & (a.lpr - 1), worker = threadIdx.x / a.lpr, workers = kEmbedThreads / a.lpr;
   const int col = (blockIdx.y * a.lpr + lane) * VEC;
-  Vec<VEC> acc{};
-  if (col < a.width) {
-    if (worker == 0) acc = load_vec<VEC>(a.tail + (long long)chunk * a.width + col);
-#pragma unroll 4
-    for (int c = chunk + 1 + worker; c <= last; c += workers) {
-      const Vec<VEC> h = load_vec<VEC>(a.head + (long long)c * a.width + col);
+  const bool on = col < a.width;
+  const int chunk0 = blockIdx.x * workers, chunk = chunk0 + worker;
+  auto add = [](Vec<VEC>& x, const Vec<VEC>& y) {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) acc.v[j] += h.v[j];
+    for (int j = 0; j < VEC; ++j) x.v[j] += y.v[j];
+  };
+  auto finish = [&](int run, Vec<VEC> s) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) s.v[j] *= a.scale;
+    store_vec<VEC>(a.grad_table + (long long)run * a.width + col, s);
+  };
+  int is_long = -1;
+  if (chunk < a.n_chunks - 1) {
+    const int p0 = chunk * a.chunk, p1 = p0 + a.chunk, run = a.sorted[p1 - 1];
+    // the run goes on behind this chunk and starts in it
+    if (a.sorted[p1] == run && (unsigned)run < (unsigned)a.n_rows && (p0 == 0 || a.sorted[p0 - 1] != run)) {
+      const int far = chunk + 1 + kShortRun;
+      if (far < a.n_chunks && a.sorted[far * a.chunk] == run) {
+        is_long = run;
+      } else if (on) {
+        Vec<VEC> s = load_vec<VEC>(a.tail + (long long)chunk * a.width + col);
+        bool more = true;
+        for (int c = chunk + 1; c < far && more; ++c) {
+          add(s, load_vec<VEC>(a.head + (long long)c * a.width + col));
+          more = c < a.n_chunks - 1 && a.sorted[(c + 1) * a.chunk] == run;
+        }
+        finish(run, s);
+      }
     }
   }
-  part[threadIdx.x] = acc;
-  __syncthreads();
-  for (int o = workers >> 1; o > 0; o >>= 1) {
-    if (worker < o)
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) part[threadIdx.x].v[j] += part[threadIdx.x + o * a.lpr].v[j];
+  if (lane == 0) long_run[worker] = is_long;
+  if (!__syncthreads_or(is_long >= 0)) return;
+  for (int w = 0; w < workers; ++w) {
+    const int run = long_run[w], first = chunk0 + w;
+    if (run < 0) continue;  // the same for every thread
+    int lo = first + 1 + kShortRun, hi = a.n_chunks - 1;  // last chunk that begins inside the run
+    while (lo < hi) {
+      const int mid = lo + (hi - lo + 1) / 2;
+      if (a.sorted[mid * a.chunk] == run) lo = mid;
+      else hi = mid - 1;
+    }
+    Vec<VEC> s{};
+    if (on) {
+      if (worker == 0) s = load_vec<VEC>(a.tail + (long long)first * a.width + col);
+#pragma unroll 4
+      for (int c = first + 1 + worker; c <= lo; c += workers) add(s, load_vec<VEC>(a.head + (long long)c * a.width + col));
+    }
+    part[threadIdx.x] = s;
     __syncthreads();
-  }
-  if (worker == 0 && col < a.width) {
-    acc = part[threadIdx.x];
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) acc.v[j] *= a.scale;
-    store_vec<VEC>(a.grad_table + (long long)run * a.width + col, acc);
+    for (int o = workers >> 1; o > 0; o >>= 1) {
+      if (worker < o) add(part[threadIdx.x], part[threadIdx.x + o * a.lpr]);
+      __syncthreads();
+    }
+    if (worker == 0 && on) finish(run, part[threadIdx.x]);
+    __syncthreads();
   }
 }
 
@@ -400,21 +529,39 @@ int embed_chunk(int n, int width) {
 }  // namespace
 
 size_t token_sort_workspace(int n, int n_rows) {
+  if (n <= kBlockTokens) return 0;
   const int p = sort_passes(n_rows);
   const size_t counts = sizeof(int) * (size_t)(sort_tiles(n) + 1) * kDigits;
-  return (size_t)(p > 1 ? 2 : 1) * counts + (p > 1 ? 2 * pad256(sizeof(int) * (size_t)n) : 0);
+  return (size_t)p * counts + (p > 1 ? 2 * pad256(sizeof(int) * (size_t)n) : 0);
 }
 
-cudaError_t launch_token_sort(int n, int n_rows, const int* tokens, int* order, int* sorted, void* ws, cudaStream_t stream) {
+template <int ITEMS>
+static cudaError_t sort_block(int n, int n_rows, int passes, const int* tokens, int* order, int* sorted,
+                              cudaStream_t stream) {
+  constexpr int bytes = sizeof(int) * (2 * kBlockThreads * ITEMS + kBlockThreads / 32 * kDigits);
+  const cudaError_t e =
+      cudaFuncSetAttribute(sort_block_kernel<ITEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e != cudaSuccess) return e;
+  sort_block_kernel<ITEMS><<<1, kBlockThreads, bytes, stream>>>(n, n_rows, passes, tokens, order, sorted);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_token_sort(int n, int n_rows, const int* tokens, int* order, int* sorted, void* ws,
+                              cudaStream_t stream) {
   if (n == 0) return cudaSuccess;
   const int passes = sort_passes(n_rows);
+  if (n <= kBlockTokens) {
+    // as few positions a thread as hold the tokens
+    if (n <= kBlockThreads) return sort_block<1>(n, n_rows, passes, tokens, order, sorted, stream);
+    if (n <= 4 * kBlockThreads) return sort_block<4>(n, n_rows, passes, tokens, order, sorted, stream);
+    return sort_block<kBlockItems>(n, n_rows, passes, tokens, order, sorted, stream);
+  }
   const unsigned tiles = (unsigned)sort_tiles(n);
-  const size_t counts_bytes = sizeof(int) * ((size_t)tiles + 1) * kDigits, n_bytes = pad256(sizeof(int) * (size_t)n);
-  char* at = (char*)ws;
-  int* counts[2] = {(int*)at, (int*)(at + counts_bytes)};
-  int* tmp_keys = (int*)(at + 2 * counts_bytes);
-  int* tmp_pos = (int*)(at + 2 * counts_bytes + n_bytes);
-  sort_count_kernel<<<tiles, kSortThreads, 0, stream>>>(n, n_rows, tokens, counts[0]);
+  const long long per_pass = ((long long)tiles + 1) * kDigits;
+  int* counts = (int*)ws;
+  int* tmp_keys = (int*)((char*)ws + sizeof(int) * (size_t)passes * per_pass);
+  int* tmp_pos = (int*)((char*)tmp_keys + pad256(sizeof(int) * (size_t)n));
+  sort_count_kernel<<<tiles, kSortThreads, 0, stream>>>(n, n_rows, passes, per_pass, tokens, counts);
   cudaError_t e = cudaGetLastError();
   const int *keys = nullptr, *pos = nullptr;
   for (int p = 0; p < passes && e == cudaSuccess; ++p) {
@@ -422,16 +569,12 @@ cudaError_t launch_token_sort(int n, int n_rows, const int* tokens, int* order, 
     const bool to_out = (passes - 1 - p) % 2 == 0;
     int* ko = to_out ? sorted : tmp_keys;
     int* po = to_out ? order : tmp_pos;
-    int* next = p + 1 < passes ? counts[(p + 1) & 1] : nullptr;
-    if (next != nullptr) e = cudaMemsetAsync(next, 0, sizeof(int) * (size_t)tiles * kDigits, stream);
-    if (e == cudaSuccess && tiles > kSortScanTiles) {
-      sort_prefix_kernel<<<kDigits, kSortThreads, 0, stream>>>((int)tiles, counts[p & 1]);
-      e = cudaGetLastError();
-    }
-    if (e != cudaSuccess) break;
-    sort_scatter_kernel<<<tiles, kSortThreads, 0, stream>>>(n, n_rows, 8 * p, tokens, keys, pos, counts[p & 1], ko, po,
-                                                            next);
-    e = cudaGetLastError();
+    int* here = counts + p * per_pass;
+    if (tiles > kSortScanTiles)
+      e = launch_kernel(sort_prefix_kernel, dim3(kDigits), dim3(kSortThreads), 0, stream, true, (int)tiles, here);
+    if (e == cudaSuccess)
+      e = launch_kernel(sort_scatter_kernel, dim3(tiles), dim3(kSortThreads), 0, stream, true, n, n_rows, 8 * p, tokens,
+                        keys, pos, (const int*)here, ko, po, p + 1 < passes ? here + per_pass : (int*)nullptr);
     keys = ko;
     pos = po;
   }
@@ -468,11 +611,12 @@ static cudaError_t embed_bwd(EmbedBwdArgs a, cudaStream_t stream) {
   long long clear = ((long long)a.n_rows + kEmbedThreads - 1) / kEmbedThreads;
   if (clear > 1024) clear = 1024;
   if (blocks + clear > 0x7fffffffLL || a.slices > 65535) return cudaErrorInvalidValue;
-  embed_bwd_kernel<VEC><<<(unsigned)(blocks + clear), kEmbedThreads, 0, stream>>>(a, (int)blocks);
-  cudaError_t e = cudaGetLastError();
+  embed_bwd_kernel<VEC><<<(unsigned)(blocks + clear), kEmbedThreads, 0, stream>>>(a, (int)clear);
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.n_chunks < 2) return e;
-  embed_join_kernel<VEC><<<dim3((unsigned)(a.n_chunks - 1), (unsigned)a.slices), kEmbedThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const int workers = kEmbedThreads / a.lpr;
+  return launch_kernel(embed_join_kernel<VEC>, dim3((unsigned)((a.n_chunks - 2) / workers + 1), (unsigned)a.slices),
+                       dim3(kEmbedThreads), 0, stream, true, a);
 }
 
 cudaError_t launch_embed_bwd(int n, int n_rows, int width, const int* order, const int* sorted, const float* grad_out,

@@ -221,4 +221,4 @@ def test_refusals(api):
     with pytest.raises(CGTPError):
         api.token_sort(tok, -1)
     with pytest.raises(CGTPError):
-        api.token_sort(tok, 3, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+        api.token_sort(tok.repeat(5000), 3, workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))

@@ -87,9 +87,9 @@ def test_host_errors():
     assert L.cgtp_token_sort(4, 4, P, P, other, P, big, None) == 1
     assert L.cgtp_token_sort(4, 4, P, other, other, P, big, None) == 1
     third = ctypes.c_void_p(0x3000)
-    assert L.cgtp_token_sort(4, 4, P, other, third, None, 0, None) == 7
-    assert L.cgtp_token_sort(4, 4, P, other, third, P, 8, None) == 7
-    assert L.cgtp_token_sort(4, 4, P, other, third, bad, big, None) == 1          # misaligned workspace
+    assert L.cgtp_token_sort(10000, 4, P, other, third, None, 0, None) == 7
+    assert L.cgtp_token_sort(10000, 4, P, other, third, P, 8, None) == 7
+    assert L.cgtp_token_sort(10000, 4, P, other, third, bad, big, None) == 1      # misaligned workspace
     # embedding
     assert L.cgtp_embed_forward(4, 4, 8, P, None, f(1), P, 8, None) == 1
     assert L.cgtp_embed_forward(4, 4, 8, P, P, f(1), P, 7, None) == 1             # rows would overlap
