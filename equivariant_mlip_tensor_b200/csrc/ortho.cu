@@ -35,7 +35,9 @@ constexpr double kNsEps = 1e-7;
 // X, each its own columns, as fp16 pairs in shared memory from the first step
 // to the last; A and then b A + c A A (at most 128 x 128) are in every block.
 // The same tile of X is read along its rows for X X^T and down its rows for
-// the last product.  With more than one block, the blocks' parts of X X^T meet
+// the last product.  Between the products the fp32 values of A and X stay in tensor
+// memory beside the accumulators, each thread its own, so that only operands
+// are converted.  With more than one block, the blocks' parts of X X^T meet
 // in cluster shared memory: each block sums its share of the entries over the
 // blocks in a fixed order and writes it to all.
 //
@@ -133,8 +135,12 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
   const int c0 = rank * a.nj;
   const float* g = a.g + (long long)matrix * a.rows * a.cols;
   float* out = a.out + (long long)matrix * a.rows * a.cols;
+  // tensor memory: the accumulators of X X^T, then A in place of the first and R R behind it, then P X over both;
+  // and X
+  const int square_at = a.mp * (a.parts > 1 ? a.parts - 1 : 1);
+  const int x_at = square_at + a.mp > a.nj ? square_at + a.mp : a.nj;
   uint32_t columns = 32;
-  while ((int)columns < a.mp * a.parts || (int)columns < a.nj) columns <<= 1;
+  while ((int)columns < x_at + a.nj) columns <<= 1;
 
   if (issuer) {
     tc::tmem_alloc(tc::smem_addr(&tmem_slot), columns);
@@ -223,7 +229,7 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
         for (int k = 0; k < 3; ++k) tc::cluster_sync();
       }
       wait_ready();
-      issue_products(tmem, a_k, a_k, al, al, jump, 2, jump, 0, a.mp / 16, square, issue);
+      issue_products(tmem + square_at, a_k, a_k, al, al, jump, 2, jump, 0, a.mp / 16, square, issue);
       tc::commit(done, issue);
       wait_ready();
       issue_products(tmem, a_k, x_mn, al, xl, jump, 128, 0, 0, a.mp / 16, wide, issue);
@@ -251,70 +257,88 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
       if (ok) ok = tc::mbar_wait(ready, ready_parity);
       ready_parity ^= 1;
     };
-    // f(column, 8 values) for the thread's columns below `end`; `parts` accumulators are added
-    auto for_columns = [&](int end, int parts, auto&& f) {
+    // f(column, 16 values of the accumulator, 16 values kept at `kept`) for the thread's columns below `end`;
+    // `parts` accumulators `at`, at + mp, ... are added
+    auto for_columns = [&](int end, int at, int parts, int kept, auto&& f) {
       if (!live) return;
       for (int c = first; c < end; c += 64) {
-        uint32_t p[16];
-        tc::tmem_load16(t_row + c, p);
+        uint32_t p[16], q[16];
+        tc::tmem_load16(t_row + at + c, p);
+        if (kept >= 0) tc::tmem_load16(t_row + kept + c, q);
         tc::tmem_wait(p);
-        float2 w[8];
+        if (kept >= 0) tc::tmem_wait(q);
+        float2 w[8], x[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = make_float2(__uint_as_float(p[2 * i]), __uint_as_float(p[2 * i + 1]));
+        for (int i = 0; i < 8; ++i) {
+          w[i] = make_float2(__uint_as_float(p[2 * i]), __uint_as_float(p[2 * i + 1]));
+          x[i] = make_float2(__uint_as_float(q[2 * i]), __uint_as_float(q[2 * i + 1]));
+        }
         for (int k = 1; k < parts; ++k) {
-          tc::tmem_load16(t_row + k * a.mp + c, p);
+          tc::tmem_load16(t_row + at + k * a.mp + c, p);
           tc::tmem_wait(p);
 #pragma unroll
           for (int i = 0; i < 8; ++i)
             w[i] = __fadd2_rn(w[i], make_float2(__uint_as_float(p[2 * i]), __uint_as_float(p[2 * i + 1])));
         }
-        if (row_on) {
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float2 u[4] = {w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
-            f(c + 8 * h, u);
-          }
-        }
+        f(c, w, x);
         __syncwarp();
       }
     };
-    // the element of column `col` out of eight, which becomes 0
-    auto take = [](float2(&w)[4], int col) {
+    // the element of column `col` out of sixteen, which becomes 0
+    auto take = [](float2(&w)[8], int col) {
       float d = 0.f;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < 8; ++i) {
         if (col == 2 * i) d = w[i].x, w[i].x = 0.f;
         if (col == 2 * i + 1) d = w[i].y, w[i].y = 0.f;
       }
       return d;
     };
-    auto place = [&](int c) { return (c >> 6) * row_set + tc::tile_unit(r, (c >> 3) & 7); };
-    auto put = [&](uint8_t* tiles, int set, uint32_t at, const float2(&w)[4]) {
-      uint4 hi, lo;
-      tc::split8(w, hi, lo);
-      *reinterpret_cast<uint4*>(tiles + at) = hi;
-      *reinterpret_cast<uint4*>(tiles + set + at) = lo;
+    // 16 columns from c on to and from the tiles
+    auto place = [&](int c, int h) { return (c >> 6) * row_set + tc::tile_unit(r, ((c >> 3) + h) & 7); };
+    auto put = [&](uint8_t* tiles, int set, int c, const float2(&w)[8]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float2 u[4] = {w[4 * h], w[4 * h + 1], w[4 * h + 2], w[4 * h + 3]};
+        uint4 hi, lo;
+        tc::split8(u, hi, lo);
+        const uint32_t at = place(c, h);
+        *reinterpret_cast<uint4*>(tiles + at) = hi;
+        *reinterpret_cast<uint4*>(tiles + set + at) = lo;
+      }
     };
-    auto get = [&](const uint8_t* tiles, int set, uint32_t at, float2(&w)[4]) {
-      tc::join8(*reinterpret_cast<const uint4*>(tiles + at), *reinterpret_cast<const uint4*>(tiles + set + at), w);
+    auto get = [&](const uint8_t* tiles, int set, int c, float2(&w)[8]) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t at = place(c, h);
+        float2 u[4];
+        tc::join8(*reinterpret_cast<const uint4*>(tiles + at), *reinterpret_cast<const uint4*>(tiles + set + at), u);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[4 * h + i] = u[i];
+      }
     };
     auto pair = [](float v) { return make_float2(v, v); };
 
     for (int step = 0; step < a.steps; ++step) {
       // A = X X^T: the diagonal to a_diag, the rest (x 2^14) to the tiles
       wait_done();
-      for_columns(a.mp, a.parts, [&](int c, float2(&w)[4]) {
+      for_columns(a.mp, 0, a.parts, -1, [&](int c, float2(&w)[8], float2(&)[8]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __fmul2_rn(w[i], pair(1.f / kXScale));
+        for (int i = 0; i < 8; ++i) w[i] = __fmul2_rn(w[i], pair(1.f / kXScale));
         if (blocks > 1) {
-          float4* to = reinterpret_cast<float4*>(part + r * L.part_stride + c);
-          to[0] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
-          to[1] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
-        } else {
-          if ((r >> 3) == (c >> 3)) a_diag[r] = take(w, r & 7) * (1.f / kXScale);
-          put(as, L.a_set, place(c), w);
+          if (row_on) {
+            float4* to = reinterpret_cast<float4*>(part + r * L.part_stride + c);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) to[i] = make_float4(w[2 * i].x, w[2 * i].y, w[2 * i + 1].x, w[2 * i + 1].y);
+          }
+          return;
         }
+        const float d = (r >> 4) == (c >> 4) ? take(w, r & 15) : 0.f;
+        if ((r >> 4) == (c >> 4) && row_on) a_diag[r] = d * (1.f / kXScale);
+        tc::tmem_store16(t_row + c, w);
+        if (row_on) put(as, L.a_set, c, w);
       });
+      if (blocks == 1) tc::tmem_store_wait();
       if (blocks > 1) {
         __syncwarp();
         tc::cluster_sync();  // every block's part is there
@@ -342,8 +366,15 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
               w[i].x += __shfl_xor_sync(0xffffffffu, w[i].x, o);
               w[i].y += __shfl_xor_sync(0xffffffffu, w[i].y, o);
             }
-          if (q < pairs && rr / 8 == cu)
-            tc::peer_store(tc::peer_addr(tc::smem_addr(&a_diag[rr]), peer), take(w, rr & 7) * (1.f / kXScale));
+          if (q < pairs && rr / 8 == cu) {
+            float d = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if ((rr & 7) == 2 * i) d = w[i].x, w[i].x = 0.f;
+              if ((rr & 7) == 2 * i + 1) d = w[i].y, w[i].y = 0.f;
+            }
+            tc::peer_store(tc::peer_addr(tc::smem_addr(&a_diag[rr]), peer), d * (1.f / kXScale));
+          }
           tc::split8(w, hi[k], lo[k]);
         }
         __syncwarp();
@@ -367,25 +398,26 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
       wait_done();
       all_wrote();
       const float dr = row_on ? a_diag[r] : 0.f;
-      for_columns(a.mp, 1, [&](int c, float2(&w)[4]) {
-        const uint32_t at = place(c);
-        float2 x[4];
-        get(as, L.a_set, at, x);
-        if ((r >> 3) == (c >> 3)) {
-          float2 y[4] = {w[0], w[1], w[2], w[3]};
-          p_diag[r] = fmaf(kNsC, fmaf(dr, dr, take(y, r & 7) * (1.f / (kXScale * kXScale))), kNsB * dr);
+      for_columns(a.mp, square_at, 1, blocks == 1 ? 0 : -1, [&](int c, float2(&w)[8], float2(&x)[8]) {
+        if (!row_on) return;
+        if (blocks > 1) get(as, L.a_set, c, x);
+        const bool diagonal = (r >> 4) == (c >> 4);
+        if (diagonal) {
+          const float d = take(w, r & 15) * (1.f / (kXScale * kXScale));
+          p_diag[r] = fmaf(kNsC, fmaf(dr, dr, d), kNsB * dr);
         }
-        const float4 d0 = *reinterpret_cast<const float4*>(a_diag + c), d1 = *reinterpret_cast<const float4*>(a_diag + c + 4);
-        const float2 dc[4] = {make_float2(d0.x, d0.y), make_float2(d0.z, d0.w), make_float2(d1.x, d1.y),
-                              make_float2(d1.z, d1.w)};
         constexpr float k = kPScale / kXScale;
+        const float own = k * fmaf(kNsC, dr, kNsB);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float2 by = __ffma2_rn(dc[i], pair(k * kNsC), pair(k * fmaf(kNsC, dr, kNsB)));
-          w[i] = __ffma2_rn(w[i], pair(k / kXScale * kNsC), __fmul2_rn(x[i], by));
+        for (int i = 0; i < 8; i += 2) {
+          const float4 d = *reinterpret_cast<const float4*>(a_diag + c + 2 * i);
+          const float2 y0 = __ffma2_rn(make_float2(d.x, d.y), pair(k * kNsC), pair(own));
+          const float2 y1 = __ffma2_rn(make_float2(d.z, d.w), pair(k * kNsC), pair(own));
+          w[i] = __ffma2_rn(w[i], pair(k / kXScale * kNsC), __fmul2_rn(x[i], y0));
+          w[i + 1] = __ffma2_rn(w[i + 1], pair(k / kXScale * kNsC), __fmul2_rn(x[i + 1], y1));
         }
-        if ((r >> 3) == (c >> 3)) take(w, r & 7);
-        put(as, L.a_set, at, w);
+        // on the diagonal both terms are zero: x was taken there before, w just now
+        put(as, L.a_set, c, w);
       });
       wrote();
       // X = (a + diagonal of P) X + (the rest of P) X
@@ -393,33 +425,33 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
       all_wrote();
       const float dx = row_on ? kNsA + p_diag[r] : 0.f;
       const bool last = step + 1 == a.steps;
-      for_columns(a.nj, 1, [&](int c, float2(&w)[4]) {
-        const uint32_t at = place(c);
-        float2 x[4];
-        get(xs, L.x_set, at, x);
+      for_columns(a.nj, 0, 1, step > 0 ? x_at : -1, [&](int c, float2(&w)[8], float2(&x)[8]) {
+        if (step == 0 && row_on) get(xs, L.x_set, c, x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w[i] = __ffma2_rn(w[i], pair(1.f / kPScale), __fmul2_rn(x[i], pair(dx)));
+        for (int i = 0; i < 8; ++i) w[i] = __ffma2_rn(w[i], pair(1.f / kPScale), __fmul2_rn(x[i], pair(dx)));
         if (!last) {
-          put(xs, L.x_set, at, w);
+          tc::tmem_store16(t_row + x_at + c, w);
+          if (row_on) put(xs, L.x_set, c, w);
         } else if (r < a.m) {
           const int col = c0 + c;
           const float by = ok ? a.scale / kXScale : __int_as_float(0x7fffffff);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[i] = __fmul2_rn(w[i], pair(by));
-          if (a.vec4 && col + 8 <= a.n) {
+          for (int i = 0; i < 8; ++i) w[i] = __fmul2_rn(w[i], pair(by));
+          if (a.vec4 && col + 16 <= a.n) {
             float4* to = reinterpret_cast<float4*>(out + (long long)r * a.cols + col);
-            to[0] = make_float4(w[0].x, w[0].y, w[1].x, w[1].y);
-            to[1] = make_float4(w[2].x, w[2].y, w[3].x, w[3].y);
-          } else {
-            const float o[8] = {w[0].x, w[0].y, w[1].x, w[1].y, w[2].x, w[2].y, w[3].x, w[3].y};
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
+            for (int i = 0; i < 4; ++i) to[i] = make_float4(w[2 * i].x, w[2 * i].y, w[2 * i + 1].x, w[2 * i + 1].y);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
               if (col + i < a.n)
-                out[a.tall ? (long long)(col + i) * a.cols + r : (long long)r * a.cols + col + i] = o[i];
+                out[a.tall ? (long long)(col + i) * a.cols + r : (long long)r * a.cols + col + i] =
+                    i & 1 ? w[i / 2].y : w[i / 2].x;
           }
         }
       });
       if (!last) {
+        tc::tmem_store_wait();
         wrote();
         all_wrote();
       }
@@ -454,7 +486,7 @@ cudaError_t launch_small(int batch, int rows, int cols, int steps, float scale, 
   a.nj = ((a.n + blocks - 1) / blocks + 15) / 16 * 16;
   // Sums of like signs (the diagonal) lose half a step each time 16 columns are
   // added: accumulators of some 64 columns, added in fp32, keep that small.  256
-  // columns of tensor memory at most, so that two blocks fit an SM.
+  // columns of tensor memory for them at most, X takes the others.
   a.parts = a.nj / 64 < 256 / a.mp ? a.nj / 64 : 256 / a.mp;
   a.parts = a.parts < 1 ? 1 : a.parts > 4 ? 4 : a.parts;
   a.vec4 = !a.tall && cols % 4 == 0 && (((uintptr_t)g | (uintptr_t)out) & 15u) == 0;

@@ -89,6 +89,17 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&r)[16]) {
                : "memory");
 }
 
+// The counterpart: 16 columns of the warp's lanes written; tmem_store_wait before they are read again.
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const float2 (&v)[8]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(addr),
+      "f"(v[0].x), "f"(v[0].y), "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y),
+      "f"(v[4].x), "f"(v[4].y), "f"(v[5].x), "f"(v[5].y), "f"(v[6].x), "f"(v[6].y), "f"(v[7].x), "f"(v[7].y)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
 // ---- operands: tiles of rows x 64 fp16 (128 bytes a row), 128-byte swizzle
 // (16-byte unit u of row r lies at u ^ (r & 7)), base on a 1024-byte boundary.
 // Read along the row (K-major) or down the rows (MN-major) from the same bytes.
