@@ -37,9 +37,11 @@ constexpr double kNsEps = 1e-7;
 // The same tile of X is read along its rows for X X^T and down its rows for
 // the last product.  Between the products the fp32 values of A and X stay in tensor
 // memory beside the accumulators, each thread its own, so that only operands
-// are converted.  With more than one block, the blocks' parts of X X^T meet
-// in cluster shared memory: each block sums its share of the entries over the
-// blocks in a fixed order and writes it to all.
+// are converted.  With more than one block, each sends its part of
+// X X^T to the blocks that own the entries, which sum them in a fixed order and
+// send A to all: stores that count their bytes on the receiver's mbarrier, so a
+// block waits for its data alone (barriers of the whole cluster around loads from
+// the other blocks took 4 us a step at 64 x 1920).
 //
 // The diagonals of A and of P = b A + c A A stay out of the operands and are
 // applied in fp32: with A = D + R, A A = D D + D R + R D + R R, and P X likewise.
@@ -61,22 +63,21 @@ struct SmallArgs {
   float* out;
 };
 
-// Shared memory of a block: X as two sets of 64-column tiles, then A (two sets
-// again), whose place the fp32 parts of X X^T take before A is known; a full
-// set of 128 rows behind the last tile is always inside the allocation,
-// because an operand of M = 128 rows reads that far (those rows of the result
-// are not used).
+// Shared memory of a block: X as two sets of 64-column tiles, then A as two sets,
+// then the fp32 parts that a block of a cluster receives: [block][its units of
+// 8 columns]; a full set of 128 rows behind the last tile is always inside the
+// allocation, because an operand of M = 128 rows reads that far (those rows of
+// the result are not used).
 struct SmallLayout {
-  int x_set, a_set, part_stride, bytes;
+  int x_set, a_set, part_at, bytes;
 };
 __host__ __device__ inline SmallLayout small_layout(int mp, int nj, int blocks) {
   SmallLayout L;
   L.x_set = (nj + 63) / 64 * mp * 128;
   L.a_set = (mp + 63) / 64 * mp * 128;
-  L.part_stride = mp + 4;  // floats: rows 16 bytes apart modulo 128, no bank conflicts of 16-byte stores
-  const int part = blocks > 1 ? mp * L.part_stride * 4 : 0;
-  const int a_bytes = 2 * L.a_set > part ? 2 * L.a_set : part;
-  L.bytes = 2 * L.x_set + a_bytes + (kSmallSide - mp) * 128 + 1024;
+  L.part_at = 2 * L.x_set + 2 * L.a_set;
+  const int part = blocks > 1 ? mp * mp * 4 : 0, over = (kSmallSide - mp) * 128;
+  L.bytes = L.part_at + (part > over ? part : over) + 1024;
   return L;
 }
 
@@ -121,14 +122,14 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
   __shared__ __align__(16) float a_diag[kSmallSide];  // diagonal of A
   __shared__ float p_diag[kSmallSide];  // diagonal of P
   __shared__ uint32_t tmem_slot;
-  __shared__ uint64_t bars[2];
+  __shared__ uint64_t bars[4];
   const SmallLayout L = small_layout(a.mp, a.nj, blocks);
   uint8_t* base = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
   uint8_t* xs = base;
   uint8_t* as = base + 2 * L.x_set;
-  float* part = reinterpret_cast<float*>(as);
   const uint32_t x_addr = tc::smem_addr(xs), a_addr = tc::smem_addr(as);
   const uint32_t done = tc::smem_addr(&bars[0]), ready = tc::smem_addr(&bars[1]);
+  const uint32_t parts_in = tc::smem_addr(&bars[2]), a_in = tc::smem_addr(&bars[3]);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const bool issuer = warp == kSmallThreads / 32;
   const int rank = blockIdx.x % blocks, matrix = blockIdx.x / blocks;
@@ -147,6 +148,8 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
     if (lane == 0) {
       tc::mbar_init(done, 1);
       tc::mbar_init(ready, kSmallThreads / 32);
+      tc::mbar_init(parts_in, 1);
+      tc::mbar_init(a_in, 1);
     }
   }
   // X once from memory; the Frobenius norm from squares in 64 bits, which
@@ -224,10 +227,6 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
         issue_products(tmem + p * a.mp, x_k, x_k, xl, xl, jump, 2, jump, p * (a.nj / 16) / a.parts,
                        (p + 1) * (a.nj / 16) / a.parts, square, issue);
       tc::commit(done, issue);
-      if (blocks > 1) {
-        __syncwarp();
-        for (int k = 0; k < 3; ++k) tc::cluster_sync();
-      }
       wait_ready();
       issue_products(tmem + square_at, a_k, a_k, al, al, jump, 2, jump, 0, a.mp / 16, square, issue);
       tc::commit(done, issue);
@@ -318,19 +317,34 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
       }
     };
     auto pair = [](float v) { return make_float2(v, v); };
+    const int own_units = a.mp * a.mp / 8 / blocks;  // 8-column units of A that a block sums
+    const uint32_t part_addr = tc::smem_addr(base) + L.part_at;
 
     for (int step = 0; step < a.steps; ++step) {
+      if (blocks > 1 && tid == 0) {  // what this step will receive
+        tc::mbar_expect(parts_in, own_units * blocks * 32);
+        tc::mbar_expect(a_in, 4 * a.mp * a.mp + 4 * a.mp);
+      }
       // A = X X^T: the diagonal to a_diag, the rest (x 2^14) to the tiles
       wait_done();
       for_columns(a.mp, 0, a.parts, -1, [&](int c, float2(&w)[8], float2(&)[8]) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) w[i] = __fmul2_rn(w[i], pair(1.f / kXScale));
-        if (blocks > 1) {
-          if (row_on) {
-            float4* to = reinterpret_cast<float4*>(part + r * L.part_stride + c);
+        if (blocks > 1) {  // to the block that owns the unit
+          if (row_on)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) to[i] = make_float4(w[2 * i].x, w[2 * i].y, w[2 * i + 1].x, w[2 * i + 1].y);
-          }
+            for (int h = 0; h < 2; ++h) {
+              const int u = r * (a.mp / 8) + (c >> 3) + h, owner = u / own_units;
+              const uint32_t to =
+                  tc::peer_addr(part_addr + (rank * own_units + u - owner * own_units) * 32, owner);
+              const uint32_t bar = tc::peer_addr(parts_in, owner);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) {
+                const float2 x = w[4 * h + 2 * i], y = w[4 * h + 2 * i + 1];
+                tc::async_store16(to + 16 * i, make_uint4(__float_as_uint(x.x), __float_as_uint(x.y),
+                                                          __float_as_uint(y.x), __float_as_uint(y.y)), bar);
+              }
+            }
           return;
         }
         const float d = (r >> 4) == (c >> 4) ? take(w, r & 15) : 0.f;
@@ -340,23 +354,21 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
       });
       if (blocks == 1) tc::tmem_store_wait();
       if (blocks > 1) {
-        __syncwarp();
-        tc::cluster_sync();  // every block's part is there
-        // `blocks` neighbouring lanes take one 8-column unit of this block's share: each reads one block's part,
-        // all get the sum, and each writes it to one block
-        const int row_units = a.mp / 8, all = a.mp * row_units;
-        const int u0 = rank * all / blocks, pairs = ((rank + 1) * all / blocks - u0) * blocks;
-        const int peer = tid % blocks;
+        if (ok) ok = tc::mbar_wait_cluster(parts_in, step & 1);  // every block's part is there
+        // `blocks` neighbouring lanes take one unit of 8 columns: each reads one block's part, all get the
+        // sum, and each sends it to one block
+        const int row_units = a.mp / 8, pairs = own_units * blocks, peer = tid % blocks;
+        const uint32_t bar = tc::peer_addr(a_in, peer);
         constexpr int kPairs = kSmallSide * kSmallSide / 8 / kSmallThreads;
-        uint4 hi[kPairs], lo[kPairs];
 #pragma unroll
         for (int k = 0; k < kPairs; ++k) {
           if (k * kSmallThreads >= pairs) break;
-          const int q = tid + k * kSmallThreads, u = u0 + q / blocks, rr = u / row_units, cu = u % row_units;
+          const int q = tid + k * kSmallThreads, own = q / blocks, u = rank * own_units + own;
+          const int rr = u / row_units, cu = u % row_units;
           float2 w[4] = {};
           if (q < pairs) {
-            const uint32_t from = tc::peer_addr(a_addr + (rr * L.part_stride + cu * 8) * 4, peer);
-            const float4 x = tc::peer_load4(from), y = tc::peer_load4(from + 16);
+            const float4* from = reinterpret_cast<const float4*>(base + L.part_at + (peer * own_units + own) * 32);
+            const float4 x = from[0], y = from[1];
             w[0] = make_float2(x.x, x.y), w[1] = make_float2(x.z, x.w);
             w[2] = make_float2(y.x, y.y), w[3] = make_float2(y.z, y.w);
           }
@@ -366,32 +378,24 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
               w[i].x += __shfl_xor_sync(0xffffffffu, w[i].x, o);
               w[i].y += __shfl_xor_sync(0xffffffffu, w[i].y, o);
             }
-          if (q < pairs && rr / 8 == cu) {
-            float d = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if ((rr & 7) == 2 * i) d = w[i].x, w[i].x = 0.f;
-              if ((rr & 7) == 2 * i + 1) d = w[i].y, w[i].y = 0.f;
-            }
-            tc::peer_store(tc::peer_addr(tc::smem_addr(&a_diag[rr]), peer), d * (1.f / kXScale));
-          }
-          tc::split8(w, hi[k], lo[k]);
-        }
-        __syncwarp();
-        tc::cluster_sync();  // every part has been read: A may take its place
-#pragma unroll
-        for (int k = 0; k < kPairs; ++k) {
-          if (k * kSmallThreads >= pairs) break;
-          const int q = tid + k * kSmallThreads, u = u0 + q / blocks, rr = u / row_units, cu = u % row_units;
           if (q < pairs) {
+            if (rr / 8 == cu) {
+              float d = 0.f;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                if ((rr & 7) == 2 * i) d = w[i].x, w[i].x = 0.f;
+                if ((rr & 7) == 2 * i + 1) d = w[i].y, w[i].y = 0.f;
+              }
+              tc::async_store4(tc::peer_addr(tc::smem_addr(&a_diag[rr]), peer), d * (1.f / kXScale), bar);
+            }
+            uint4 hi, lo;
+            tc::split8(w, hi, lo);
             const uint32_t to = tc::peer_addr(a_addr + (cu >> 3) * row_set + tc::tile_unit(rr, cu & 7), peer);
-            tc::peer_store16(to, hi[k]);
-            tc::peer_store16(to + L.a_set, lo[k]);
+            tc::async_store16(to, hi, bar);
+            tc::async_store16(to + L.a_set, lo, bar);
           }
         }
-        tc::fence_async_cluster();
-        __syncwarp();
-        tc::cluster_sync();
+        if (ok) ok = tc::mbar_wait_cluster(a_in, step & 1);
       }
       wrote();
       // P = b A + c A A (x 2^13) over A: (A A)[r][c] = (R R)[r][c] + (d[r] + d[c]) R[r][c] off the diagonal
@@ -464,11 +468,15 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
   if (blocks > 1) tc::cluster_sync();  // no block leaves while another may still read its shared memory
 }
 
-// Blocks per matrix: as few as hold its columns (1, 2, 4 or 8).
+// Blocks per matrix: as few as hold its columns (1, 2, 4 or 8), 0 where none do.
+constexpr int kSmallShared = 226 * 1024;  // of 227 KB; the rest for the kernel's own variables
+int small_columns(int n, int blocks) { return ((n + blocks - 1) / blocks + 15) / 16 * 16; }
 int small_blocks(int m, int n) {
   if (m > kSmallSide) return 0;
-  for (int b = 1; b <= 8; b *= 2)
-    if (n <= b * kSmallColumns) return b;
+  for (int b = 1; b <= 8; b *= 2) {
+    const int nj = small_columns(n, b);
+    if (nj <= kSmallColumns && small_layout((m + 15) / 16 * 16, nj, b).bytes <= kSmallShared - 512) return b;
+  }
   return 0;
 }
 
@@ -483,7 +491,7 @@ cudaError_t launch_small(int batch, int rows, int cols, int steps, float scale, 
   a.n = a.tall ? rows : cols;
   const int blocks = small_blocks(a.m, a.n);
   a.mp = (a.m + 15) / 16 * 16;
-  a.nj = ((a.n + blocks - 1) / blocks + 15) / 16 * 16;
+  a.nj = small_columns(a.n, blocks);
   // Sums of like signs (the diagonal) lose half a step each time 16 columns are
   // added: accumulators of some 64 columns, added in fp32, keep that small.  256
   // columns of tensor memory for them at most, X takes the others.
