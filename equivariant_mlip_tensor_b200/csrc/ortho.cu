@@ -468,16 +468,21 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
   if (blocks > 1) tc::cluster_sync();  // no block leaves while another may still read its shared memory
 }
 
-// Blocks per matrix: as few as hold its columns (1, 2, 4 or 8), 0 where none do.
+// Blocks per matrix: 1, 2, 4 or 8; 0 where they cannot hold the matrix.  One
+// block as long as it holds all columns (4 x 128 x 256: 59 us, with two blocks
+// 74 us, the exchange costs more than half of the columns); then so many that
+// each has at most 128 (20 x 64 x 512: two blocks 53 us, four 44 us).
 constexpr int kSmallShared = 226 * 1024;  // of 227 KB; the rest for the kernel's own variables
 int small_columns(int n, int blocks) { return ((n + blocks - 1) / blocks + 15) / 16 * 16; }
 int small_blocks(int m, int n) {
   if (m > kSmallSide) return 0;
+  int found = 0;
   for (int b = 1; b <= 8; b *= 2) {
     const int nj = small_columns(n, b);
-    if (nj <= kSmallColumns && small_layout((m + 15) / 16 * 16, nj, b).bytes <= kSmallShared - 512) return b;
+    if (nj <= kSmallColumns && small_layout((m + 15) / 16 * 16, nj, b).bytes <= kSmallShared - 512) found = b;
+    if (found != 0 && (b == 1 || nj <= 128)) break;
   }
-  return 0;
+  return found;
 }
 
 cudaError_t launch_small(int batch, int rows, int cols, int steps, float scale, const float* g, float* out,
@@ -528,7 +533,8 @@ cudaError_t launch_small(int batch, int rows, int cols, int steps, float scale, 
 // P X reads down them.  Rows and columns beyond the matrix are zero and stay so.
 // A block has one warp that copies (kStages stages of 64 columns), one that
 // issues the products and sixteen that turn the accumulator into the next
-// operand.  The launches are dependent ones (programmatic stream serialization):
+// operand.  The diagonal of X X^T, long sums of like signs, is summed in fp32 where
+// X is made.  The launches are dependent ones (programmatic stream serialization):
 // each sets up while the one before ends and waits for it before its first
 // access to global memory.  Four accumulators fill the tensor memory: one for low high + high
 // low, three that share the columns of high high, so that no entry is rounded
@@ -545,6 +551,7 @@ struct LargeArgs {
   long long x_set, a_set;  // bytes of one set of tiles of one matrix
   uint8_t *x, *x_next, *a, *p;  // [batch][2 sets][row tiles][column tiles]
   float *a_diag, *p_diag;       // [batch][mt * 128]
+  float* squares;               // [batch][nt][mt * 128] sums of squares of X by row and 64-column tile
   double* sums;                 // [batch][kSumBlocks] sums of squares
   const float* g;
   float* out;
@@ -581,6 +588,7 @@ __global__ void __launch_bounds__(256) ortho_tiles_kernel(LargeArgs a) {
   const float s1 = ldexpf(1.f, e / 2), s2 = ldexpf(f, e - e / 2);
   const float* g = a.g + (long long)z * a.rows * a.cols;
   uint8_t* to = a.x + (2 * z * a.x_set) + ((long long)rt * a.nt + ct) * kTileBytes;
+  __shared__ float sq[8][128];
   for (int q = threadIdx.x; q < 128 * 8; q += 256) {
     const int r = a.tall ? q & 127 : q >> 3, u = a.tall ? q >> 7 : q & 7;
     const int row = rt * 128 + r, col = ct * 64 + u * 8;
@@ -598,6 +606,17 @@ __global__ void __launch_bounds__(256) ortho_tiles_kernel(LargeArgs a) {
     const uint32_t at = tc::tile_unit(r, u);
     *reinterpret_cast<uint4*>(to + at) = hi;
     *reinterpret_cast<uint4*>(to + a.x_set + at) = lo;
+    float2 d = __fmul2_rn(w[0], w[0]);
+#pragma unroll
+    for (int i = 1; i < 4; ++i) d = __ffma2_rn(w[i], w[i], d);
+    sq[u][r] = d.x + d.y;
+  }
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    float d = 0.f;
+#pragma unroll
+    for (int u = 0; u < 8; ++u) d += sq[u][threadIdx.x];
+    a.squares[((long long)z * a.nt + ct) * a.mt * 128 + rt * 128 + threadIdx.x] = d;
   }
 }
 
@@ -610,6 +629,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) ortho_product_kernel(LargeAr
   extern __shared__ uint8_t raw[];
   __shared__ uint32_t tmem_slot;
   __shared__ uint64_t bars[2 * kStages + 1];
+  __shared__ float sq[4][128];
   uint8_t* base = raw + ((1024 - (tc::smem_addr(raw) & 1023)) & 1023);
   const uint32_t smem = tc::smem_addr(base);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
@@ -711,6 +731,13 @@ __global__ void __launch_bounds__(kLargeThreads, 1) ortho_product_kernel(LargeAr
         own[k][1] = *reinterpret_cast<const uint4*>(p + set);
       }
     const float dr = MODE == kSquare ? ad[row] : MODE == kApply ? kNsA + pd[row] : 0.f;
+    if (MODE == kGram && diagonal && first == 0) {  // x 2^28
+      float d = 0.f;
+#pragma unroll 8
+      for (int k = 0; k < a.nt; ++k) d += a.squares[(z * a.nt + k) * a.mt * 128 + row];
+      a.a_diag[z * a.mt * 128 + row] = d * (1.f / (kXScale * kXScale));
+    }
+    float2 squares = make_float2(0.f, 0.f);
     ok = tc::mbar_wait(done, 0);
     tc::fence_after_sync();
     const float fine = ok ? 1.f : __int_as_float(0x7fffffff);
@@ -748,7 +775,7 @@ __global__ void __launch_bounds__(kLargeThreads, 1) ortho_product_kernel(LargeAr
         if (MODE == kGram) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) w[i] = __fmul2_rn(w[i], pair(fine / kXScale));
-          if (on_diagonal) a.a_diag[z * a.mt * 128 + row] = take(w, r & 7) * (1.f / kXScale);
+          if (on_diagonal) take(w, r & 7);
         } else {
           float2 x[4];
           tc::join8(own[2 * half + h][0], own[2 * half + h][1], x);
@@ -770,7 +797,10 @@ __global__ void __launch_bounds__(kLargeThreads, 1) ortho_product_kernel(LargeAr
             if (on_diagonal) take(w, r & 7);
           } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __ffma2_rn(w[i], pair(fine / kPScale), __fmul2_rn(x[i], pair(dr)));
+            for (int i = 0; i < 4; ++i) {
+              w[i] = __ffma2_rn(w[i], pair(fine / kPScale), __fmul2_rn(x[i], pair(dr)));
+              squares = __ffma2_rn(w[i], w[i], squares);
+            }
           }
         }
         if (MODE == kApply && LAST) {
@@ -800,12 +830,18 @@ __global__ void __launch_bounds__(kLargeThreads, 1) ortho_product_kernel(LargeAr
         }
       }
     }
+    if (MODE == kApply && !LAST) sq[warp >> 2][r] = squares.x + squares.y;
   }
   tc::fence_async();
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
   if (warp == kSmallThreads / 32) tc::tmem_free(tmem, kColumns);
+  if (MODE == kApply && !LAST && tid < 128) {  // the tile's two column tiles as one
+    float* to = a.squares + (z * a.nt + 2 * ct) * a.mt * 128 + rt * 128 + tid;
+    to[0] = (sq[0][tid] + sq[1][tid]) + (sq[2][tid] + sq[3][tid]);
+    to[a.mt * 128] = 0.f;
+  }
   if (!(MODE == kApply && LAST) && tid == 0) {
     uint8_t* to = MODE == kGram    ? az + ((long long)rt * at_cols + 2 * ct) * kTileBytes
                   : MODE == kSquare ? pz + ((long long)rt * at_cols + 2 * ct) * kTileBytes
@@ -828,7 +864,7 @@ LargeLayout large_layout(int batch, int m, int n) {
   L.nt = (n + 127) / 128 * 2;
   L.x_set = (size_t)L.mt * L.nt * kTileBytes;
   L.a_set = (size_t)L.mt * L.mt * 2 * kTileBytes;
-  L.bytes = (size_t)batch * (4 * L.x_set + 4 * L.a_set + 2 * L.mt * 128 * sizeof(float) + kSumBlocks * sizeof(double));
+  L.bytes = (size_t)batch * (4 * L.x_set + 4 * L.a_set + (2 + L.nt) * L.mt * 128 * sizeof(float) + kSumBlocks * sizeof(double));
   return L;
 }
 
@@ -864,6 +900,7 @@ cudaError_t launch_large(int batch, int rows, int cols, int steps, float scale, 
   a.sums = (double*)(at += 2 * batch * L.a_set);
   a.a_diag = (float*)(a.sums + (size_t)batch * kSumBlocks);
   a.p_diag = a.a_diag + (size_t)batch * L.mt * 128;
+  a.squares = a.p_diag + (size_t)batch * L.mt * 128;
   a.g = g;
   a.out = out;
   ortho_norm_kernel<<<dim3(kSumBlocks, batch), 256, 0, stream>>>(a);
