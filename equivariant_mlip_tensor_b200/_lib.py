@@ -58,7 +58,7 @@ SIGNATURES = {
     "cgtp_embed_forward": (_i, [_i, _i, _i, _p, _p, _f, _p, _ll, _p]),
     "cgtp_embed_backward_workspace_size": (_i, [_i, _i, ctypes.POINTER(_sz)]),
     "cgtp_embed_backward": (_i, [_i, _i, _i, _p, _p, _p, _ll, _f, _p, _p, _sz, _p]),
-    "cgtp_group_norm_workspace_size": (_i, [_i, _i, _i, _i, ctypes.POINTER(_sz)]),
+    "cgtp_group_norm_workspace_size": (_i, [_i, _i, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
     "cgtp_group_norm_forward": (_i, [_i, _i, _i, _i, _p, _i, _p, _ll, _p, _p, _f, _i, _p, _ll, _p, _p, _p, _sz, _p]),
     "cgtp_group_norm_backward": (_i, [_i, _i, _i, _i, _p, _i, _p, _ll, _p, _p, _p, _p, _i, _p, _ll, _p, _ll, _p, _p,
                                       _p, _sz, _p]),

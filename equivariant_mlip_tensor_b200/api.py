@@ -249,8 +249,8 @@ def token_sort(tokens, n_rows, workspace=None):
     """Stable sort of tokens [n] into [0, n_rows) for embed_backward."""
     _check(tokens, torch.int32, "tokens")
     n, dev = tokens.numel(), tokens.device
-    order = torch.empty(n, dtype=torch.int32, device=dev)
-    srt = torch.empty(n, dtype=torch.int32, device=dev)
+    order = tokens.new_empty(n)
+    srt = torch.empty_like(order)
     ws, nb = _workspace(workspace, token_sort_workspace_bytes(n, n_rows), dev)
     _call_on(dev, "cgtp_token_sort", n, n_rows, _at(tokens), _at(order), _at(srt), _at(ws), nb)
     return TokenOrder(n_rows, order, srt)
@@ -266,7 +266,7 @@ def embed_forward(tokens, table, scale=1.0, out=None):
         raise ValueError(f"table must be [n_rows][width], got {tuple(table.shape)}")
     n, (n_rows, width), dev = tokens.numel(), table.shape, table.device
     if out is None:
-        out = torch.empty((n, width), dtype=torch.float32, device=dev)
+        out = table.new_empty((n, width))
     stride = _check_rows(out, "out", n, width)
     _same_device(dev, ("tokens", tokens), ("out", out))
     _call_on(dev, "cgtp_embed_forward", n, n_rows, width, _at(tokens), _at(table), scale, _at(out), stride)
@@ -286,7 +286,7 @@ def embed_backward(order, grad_out, scale=1.0, out=None, workspace=None):
     _check_vector(order.sorted, torch.int32, "sorted", n)
     width, dev = grad_out.shape[1], grad_out.device
     if out is None:
-        out = torch.empty((order.n_rows, width), dtype=torch.float32, device=dev)
+        out = grad_out.new_empty((order.n_rows, width))
     else:
         _check(out, torch.float32, "out")
         if tuple(out.shape) != (order.n_rows, width):
@@ -302,8 +302,8 @@ def embed_backward(order, grad_out, scale=1.0, out=None, workspace=None):
 ACTIVATIONS = {None: 0, "silu": 1}
 
 
-def group_norm_workspace_bytes(n, n_samples, channels, groups):
-    return _bytes("cgtp_group_norm_workspace_size", n, n_samples, channels, groups)
+def group_norm_workspace_bytes(n, n_samples, channels, groups, max_rows=0, backward=False):
+    return _bytes("cgtp_group_norm_workspace_size", n, n_samples, channels, groups, max_rows, int(backward))
 
 
 def _norm_shape(x, gamma, beta, groups, graph_ptr, activation):
@@ -332,12 +332,12 @@ def group_norm_forward(x, gamma, beta, groups, graph_ptr=None, eps=1e-5, activat
     n, c, b, stride = _norm_shape(x, gamma, beta, groups, graph_ptr, activation)
     dev = x.device
     if out is None:
-        out = torch.empty((n, c), dtype=torch.float32, device=dev)
+        out = torch.empty_like(x)  # rows without a gap
     out_stride = _check_rows(out, "out", n, c)
     _same_device(dev, ("gamma", gamma), ("beta", beta), ("graph_ptr", graph_ptr), ("out", out))
-    mean = torch.empty((b, groups), dtype=torch.float32, device=dev)
-    rstd = torch.empty((b, groups), dtype=torch.float32, device=dev)
-    ws, nb = _workspace(workspace, group_norm_workspace_bytes(n, b, c, groups), dev)
+    mean = x.new_empty((b, groups))
+    rstd = torch.empty_like(mean)
+    ws, nb = _workspace(workspace, group_norm_workspace_bytes(n, b, c, groups, max_rows), dev)
     _call_on(dev, "cgtp_group_norm_forward", n, b, c, groups, _at(graph_ptr), max_rows, _at(x), stride, _at(gamma),
              _at(beta), eps, ACTIVATIONS[activation], _at(out), out_stride, _at(mean), _at(rstd), _at(ws), nb)
     return out, mean, rstd
@@ -360,15 +360,15 @@ def group_norm_backward(x, gamma, beta, groups, mean, rstd, grad_y, graph_ptr=No
         grad_x = None
     else:
         if grad_x is None:
-            grad_x = torch.empty((n, c), dtype=torch.float32, device=dev)
+            grad_x = torch.empty_like(x)
         gx_stride = _check_rows(grad_x, "grad_x", n, c)
     _same_device(dev, ("gamma", gamma), ("beta", beta), ("graph_ptr", graph_ptr), ("mean", mean), ("rstd", rstd),
                  ("grad_y", grad_y), ("grad_x", grad_x))
     gg = gb = None
     if want_params:
-        gg = torch.empty(c, dtype=torch.float32, device=dev)
-        gb = torch.empty(c, dtype=torch.float32, device=dev)
-    ws, nb = _workspace(workspace, group_norm_workspace_bytes(n, b, c, groups), dev)
+        gg = x.new_empty(c)
+        gb = torch.empty_like(gg)
+    ws, nb = _workspace(workspace, group_norm_workspace_bytes(n, b, c, groups, max_rows, True), dev)
     _call_on(dev, "cgtp_group_norm_backward", n, b, c, groups, _at(graph_ptr), max_rows, _at(x), stride, _at(gamma),
              _at(beta), _at(mean), _at(rstd), ACTIVATIONS[activation], _at(grad_y), gy_stride, _at(grad_x), gx_stride,
              _at(gg), _at(gb), _at(ws), nb)

@@ -1123,19 +1123,20 @@ cgtp_status cgtp_embed_backward(int n, int n_rows, int width, const int* order, 
                                    (cudaStream_t)stream));
 }
 
-cgtp_status cgtp_group_norm_workspace_size(int n, int n_samples, int channels, int groups, size_t* bytes) {
+cgtp_status cgtp_group_norm_workspace_size(int n, int n_samples, int channels, int groups, int max_rows, int backward,
+                                           size_t* bytes) {
   if (n < 0 || n > kMaxTokens || n_samples < 0 || channels < 0 || groups < 1 || channels % groups != 0 ||
-      bytes == nullptr)
+      max_rows < 0 || bytes == nullptr)
     return CGTP_ERR_INVALID_ARG;
-  *bytes = channels == 0 ? 0 : norm_workspace(n, n_samples, channels, groups);
+  *bytes = channels == 0 ? 0 : norm_workspace(n, n_samples, channels, groups, max_rows, backward != 0);
   return CGTP_OK;
 }
 
-static cgtp_status norm_args(const NormArgs& a, int max_rows, const void* ws, size_t ws_bytes) {
+static cgtp_status norm_args(const NormArgs& a, int max_rows, bool backward, const void* ws, size_t ws_bytes) {
   size_t need = 0;
-  if (cgtp_group_norm_workspace_size(a.n, a.samples, a.channels, a.groups, &need) != CGTP_OK)
+  if (cgtp_group_norm_workspace_size(a.n, a.samples, a.channels, a.groups, max_rows, backward, &need) != CGTP_OK)
     return CGTP_ERR_INVALID_ARG;
-  if (max_rows < 0 || (a.act != CGTP_ACT_NONE && a.act != CGTP_ACT_SILU)) return CGTP_ERR_INVALID_ARG;
+  if (a.act != CGTP_ACT_NONE && a.act != CGTP_ACT_SILU) return CGTP_ERR_INVALID_ARG;
   if (a.ptr == nullptr && a.samples != 1) return CGTP_ERR_INVALID_ARG;
   if (!rows_ok(a.x, a.n, a.channels, a.x_stride)) return CGTP_ERR_INVALID_ARG;
   if (a.samples > 0 && a.channels > 0 && (a.mean == nullptr || a.rstd == nullptr)) return CGTP_ERR_INVALID_ARG;
@@ -1164,7 +1165,7 @@ cgtp_status cgtp_group_norm_forward(int n, int n_samples, int channels, int grou
   a.mean = mean;
   a.rstd = rstd;
   if (!(eps > 0.f)) return CGTP_ERR_INVALID_ARG;
-  const cgtp_status st = norm_args(a, max_rows, workspace, workspace_bytes);
+  const cgtp_status st = norm_args(a, max_rows, false, workspace, workspace_bytes);
   if (st != CGTP_OK) return st;
   if (!rows_ok(y, n, channels, y_stride) || (y == x && y_stride != x_stride)) return CGTP_ERR_INVALID_ARG;
   return launched(launch_norm_fwd(a, max_rows, workspace, (cudaStream_t)stream));
@@ -1195,7 +1196,7 @@ cgtp_status cgtp_group_norm_backward(int n, int n_samples, int channels, int gro
   a.gx_stride = gx_stride;
   a.grad_gamma = grad_gamma;
   a.grad_beta = grad_beta;
-  const cgtp_status st = norm_args(a, max_rows, workspace, workspace_bytes);
+  const cgtp_status st = norm_args(a, max_rows, true, workspace, workspace_bytes);
   if (st != CGTP_OK) return st;
   if (!rows_ok(grad_y, n, channels, gy_stride)) return CGTP_ERR_INVALID_ARG;
   if (grad_x != nullptr && (!rows_ok(grad_x, n, channels, gx_stride) || (grad_x == grad_y && gx_stride != gy_stride)))

@@ -957,13 +957,24 @@ cudaError_t norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t str
 
 }  // namespace
 
-// Enough for both directions, both splits and rows of any alignment.
-size_t norm_workspace(int n, int samples, int channels, int groups) {
+// Enough for rows of any alignment.
+size_t norm_workspace(int n, int samples, int channels, int groups, int max_rows, bool backward) {
   NormArgs a{};
+  a.n = n;
   a.samples = samples;
   a.channels = channels;
   a.groups = groups;
-  const size_t slots = (size_t)tiles_of(n, rows_per_tile(channels, 1)) + (size_t)samples + (size_t)kManyBlocks;
+  const Slabs one = fused_slabs<1>(a, max_rows, backward);
+  const Slabs four = channels % 4 == 0 ? fused_slabs<4>(a, max_rows, backward) : one;
+  const bool fused = one.count > 0 && four.count > 0;
+  if (fused && !backward) return 0;
+  const int blocks = one.blocks > four.blocks ? one.blocks : four.blocks;
+  size_t slots = (size_t)samples * (fused ? blocks : 1);
+  if (!fused) {
+    slots += (size_t)tiles_of(n, rows_per_tile(channels, 1));
+    const size_t other = (size_t)samples * blocks;  // the alignment that is fused
+    if (other > slots) slots = other;
+  }
   return terms_bytes(a) + sums_bytes(a) + pad256(sizeof(float2) * slots * (size_t)channels);
 }
 

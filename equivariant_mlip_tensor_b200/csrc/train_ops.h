@@ -41,7 +41,7 @@ struct NormArgs {
   long long gx_stride;
   float *grad_gamma, *grad_beta;  // nullable
 };
-size_t norm_workspace(int n, int samples, int channels, int groups);
+size_t norm_workspace(int n, int samples, int channels, int groups, int max_rows, bool backward);
 cudaError_t launch_norm_fwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t stream);
 cudaError_t launch_norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t stream);
 

@@ -527,13 +527,14 @@ typedef enum { CGTP_ACT_NONE = 0, CGTP_ACT_SILU = 1 } cgtp_act;
  * max_rows: a bound on the rows of a sample where the caller knows one, 0
  * otherwise; it chooses how the work is split, never the result's validity.
  * workspace: device, 256-byte aligned, of the size
- * cgtp_group_norm_workspace_size reports (for either direction).
+ * cgtp_group_norm_workspace_size reports for the same sizes, max_rows and
+ * direction (0 bytes where none is needed; NULL is accepted then).
  *
  * Backward: grad_x (nullable), grad_gamma and grad_beta ([channels], nullable),
  * all overwritten; x, gamma, beta, mean, rstd as in the forward.
  * ------------------------------------------------------------------------- */
 cgtp_status cgtp_group_norm_workspace_size(int n, int n_samples, int channels, int groups,
-                                           size_t* bytes);
+                                           int max_rows, int backward, size_t* bytes);
 cgtp_status cgtp_group_norm_forward(int n, int n_samples, int channels, int groups,
                                     const int* graph_ptr, int max_rows, const float* x,
                                     long long x_stride, const float* gamma, const float* beta,

@@ -78,8 +78,8 @@ def test_host_errors():
     assert L.cgtp_token_sort_workspace_size(4, -1, ctypes.byref(sz)) == 1
     assert L.cgtp_token_sort_workspace_size(4, 4, None) == 1
     assert L.cgtp_embed_backward_workspace_size(4, -1, ctypes.byref(sz)) == 1
-    assert L.cgtp_group_norm_workspace_size(4, 1, 12, 5, ctypes.byref(sz)) == 1   # 12 channels, 5 groups
-    assert L.cgtp_group_norm_workspace_size(4, 1, 12, 0, ctypes.byref(sz)) == 1
+    assert L.cgtp_group_norm_workspace_size(4, 1, 12, 5, 0, 0, ctypes.byref(sz)) == 1   # 12 channels, 5 groups
+    assert L.cgtp_group_norm_workspace_size(4, 1, 12, 0, 0, 0, ctypes.byref(sz)) == 1
     assert L.cgtp_orthogonalise_workspace_size(1, 8193, 4, ctypes.byref(sz)) == 1
     assert L.cgtp_orthogonalise_workspace_size(65536, 4, 4, ctypes.byref(sz)) == 1
     # token sort: missing and aliased arrays, workspace
@@ -106,7 +106,7 @@ def test_host_errors():
     assert fwd(4, 1, 8, 2, None, 0, P, 16, P, P, f(1e-5), 1, P, 8, P, P, P, big, None) == 1  # in place, other stride
     assert fwd(4, 1, 8, 2, None, -1, P, 8, P, P, f(1e-5), 1, P, 8, P, P, P, big, None) == 1
     assert fwd(4, 1, 8, 2, None, 0, P, 8, P, P, f(1e-5), 1, P, 8, None, P, P, big, None) == 1
-    assert fwd(4, 1, 8, 2, None, 0, P, 8, P, P, f(1e-5), 1, P, 8, P, P, P, 8, None) == 7
+    assert fwd(1 << 20, 1, 8, 2, None, 0, P, 8, P, P, f(1e-5), 1, P, 8, P, P, P, 8, None) == 7
     assert bwd(4, 1, 8, 2, None, 0, P, 8, P, P, P, P, 1, None, 8, P, 8, P, P, P, big, None) == 1
     assert bwd(4, 1, 8, 2, None, 0, P, 8, P, P, P, P, 1, P, 8, P, 7, P, P, P, big, None) == 1
     assert bwd(4, 1, 8, 2, None, 0, P, 8, P, P, P, P, 1, P, 8, P, 8, P, P, None, 0, None) == 7
