@@ -517,15 +517,17 @@ struct Tile {
   int lane, ty, nty, r0, r1, col, index;
   bool on;  // the thread has columns
 };
+// Tile `index` of `per` times the rows that the block's registers hold.
 template <int VEC>
-__device__ __forceinline__ Tile make_tile(const NormArgs& a, int lpr, int index) {
+__device__ __forceinline__ Tile make_tile(const NormArgs& a, int lpr, int per, int index) {
   Tile t;
   t.index = index;
   t.lane = threadIdx.x & (lpr - 1);
   t.ty = threadIdx.x / lpr;
   t.nty = kNormThreads / lpr;
-  t.r0 = index * (t.nty * kNormRows);
-  t.r1 = min(a.n - t.r0, t.nty * kNormRows) + t.r0;
+  const int rows = t.nty * kNormRows * per;
+  t.r0 = index * rows;
+  t.r1 = min(a.n - t.r0, rows) + t.r0;
   t.col = (blockIdx.y * lpr + t.lane) * VEC;
   t.on = t.col < a.channels;
   return t;
@@ -533,48 +535,60 @@ __device__ __forceinline__ Tile make_tile(const NormArgs& a, int lpr, int index)
 
 // 1, forward: slot [channel] = (mean, sum of squared deviations) of the part.
 template <int VEC>
-__global__ void __launch_bounds__(kNormThreads) norm_part_kernel(NormArgs a, int lpr, float2* __restrict__ slots) {
+__global__ void __launch_bounds__(kNormThreads) norm_part_kernel(NormArgs a, int lpr, int per, float2* __restrict__ slots) {
   __shared__ float red[VEC * kNormThreads];
   __shared__ float mean_of[VEC * 32];
-  const Tile t = make_tile<VEC>(a, lpr, blockIdx.x);
-  Vec<VEC> v[kNormRows];
-#pragma unroll
-  for (int i = 0; i < kNormRows; ++i) {
-    const int r = t.r0 + t.ty + i * t.nty;
-    v[i] = Vec<VEC>{};
-    if (t.on && r < t.r1) v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
-  }
+  const Tile t = make_tile<VEC>(a, lpr, per, blockIdx.x);
   for_parts(a, t.r0, t.r1, [&](int s, int lo, int hi) {
-    Vec<VEC> sum{};
+    // this thread's rows: count, mean, squared deviations from it
+    float count = 0.f;
+    Vec<VEC> mean{}, dev{};
+    for (int base = lo + t.ty; base < hi; base += t.nty * kNormRows) {
+      Vec<VEC> v[kNormRows], sum{}, d{};
+      float n = 0.f;
 #pragma unroll
-    for (int i = 0; i < kNormRows; ++i) {
-      const int r = t.r0 + t.ty + i * t.nty;
-      if (r >= lo && r < hi) sum = sum + v[i];
+      for (int i = 0; i < kNormRows; ++i) {
+        const int r = base + i * t.nty;
+        v[i] = Vec<VEC>{};
+        if (t.on && r < hi) v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
+      }
+#pragma unroll
+      for (int i = 0; i < kNormRows; ++i) {
+        n += base + i * t.nty < hi ? 1.f : 0.f;
+        sum = sum + v[i];
+      }
+      const Vec<VEC> m = sum * all<VEC>(1.f / n), minus = m * all<VEC>(-1.f);
+#pragma unroll
+      for (int i = 0; i < kNormRows; ++i)
+        if (base + i * t.nty < hi) {
+          const Vec<VEC> q = v[i] + minus;
+          d = fma(q, q, d);
+        }
+      // join with the rows before
+      const float both = count + n, part = n / both;
+      const Vec<VEC> q = m + mean * all<VEC>(-1.f);
+      mean = fma(q, all<VEC>(part), mean);
+      dev = fma(q * q, all<VEC>(count * part), dev + d);
+      count = both;
     }
+    Vec<VEC> sum = mean * all<VEC>(count);
     __syncthreads();
     sum_row_groups<VEC>(sum.v, red, t.ty, t.nty);
     if (t.ty == 0)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) mean_of[t.lane * VEC + j] = sum.v[j] / float(hi - lo);
     __syncthreads();
-    Vec<VEC> mean, dev{};
+    Vec<VEC> whole;
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) mean.v[j] = mean_of[t.lane * VEC + j];
-    const Vec<VEC> minus = mean * all<VEC>(-1.f);
-#pragma unroll
-    for (int i = 0; i < kNormRows; ++i) {
-      const int r = t.r0 + t.ty + i * t.nty;
-      if (r >= lo && r < hi) {
-        const Vec<VEC> q = v[i] + minus;
-        dev = fma(q, q, dev);
-      }
-    }
+    for (int j = 0; j < VEC; ++j) whole.v[j] = mean_of[t.lane * VEC + j];
+    const Vec<VEC> q = mean + whole * all<VEC>(-1.f);
+    dev = fma(q * q, all<VEC>(count), dev);
     __syncthreads();
     sum_row_groups<VEC>(dev.v, red, t.ty, t.nty);
     if (t.ty == 0 && t.on)
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
-        slots[((long long)t.index + s) * a.channels + t.col + j] = make_float2(mean.v[j], dev.v[j]);
+        slots[((long long)t.index + s) * a.channels + t.col + j] = make_float2(whole.v[j], dev.v[j]);
   });
 }
 
@@ -612,37 +626,33 @@ __global__ void __launch_bounds__(TPI > 32 ? TPI : kNormThreads)
   const float2* base = slots + ((long long)t0 + s) * a.channels + (long long)g * cpg;
   const int tid = threadIdx.x % TPI;
   auto rows_of = [&](int t) { return min(b.y, (t + 1) * rows_per_tile) - max(b.x, t * rows_per_tile); };
+  // forward: sums of n (mean - ref) and of the deviations from ref, the first part's mean; how far the whole
+  // mean is from it is taken off at the end (part means are close: little cancels)
+  const float ref = BWD || entries == 0 ? 0.f : base[0].x;
   float s1 = 0.f, s2 = 0.f;
 #pragma unroll 8
   for (long long q = tid; q < entries; q += TPI) {
     const int k = (int)(q / cpg), c = (int)(q % cpg);
     const float2 v = base[(long long)k * a.channels + c];
-    if (BWD) {
+    if constexpr (BWD) {
       const float w = a.gamma == nullptr ? 1.f : a.gamma[g * cpg + c];
       s1 = fmaf(w, v.x, s1);
       s2 = fmaf(w, v.y, s2);
     } else {
-      s1 = fmaf(float(rows_of(t0 + k)), v.x, s1);
+      const float n = float(rows_of(t0 + k)), d = v.x - ref;
+      s1 = fmaf(n, d, s1);
+      s2 += fmaf(n * d, d, v.y);
     }
   }
   s1 = item_sum<TPI>(s1, red);
-  const float mean = entries > 0 ? s1 / count : 0.f;
+  s2 = item_sum<TPI>(s2, red);
+  if (tid != 0) return;
+  const float m1 = entries > 0 ? s1 / count : 0.f, m2 = entries > 0 ? s2 / count : 0.f;
   if constexpr (BWD) {
-    s2 = item_sum<TPI>(s2, red);
-    if (tid == 0) terms[item] = make_float2(mean, entries > 0 ? s2 / count : 0.f);
+    terms[item] = make_float2(m1, m2);
   } else {
-#pragma unroll 8
-    for (long long q = tid; q < entries; q += TPI) {
-      const int k = (int)(q / cpg), c = (int)(q % cpg);
-      const float2 v = base[(long long)k * a.channels + c];
-      const float d = v.x - mean;
-      s2 += fmaf(float(rows_of(t0 + k)) * d, d, v.y);
-    }
-    s2 = item_sum<TPI>(s2, red);
-    if (tid == 0) {
-      a.mean[item] = mean;
-      a.rstd[item] = 1.f / sqrtf((entries > 0 ? s2 / count : 0.f) + a.eps);
-    }
+    a.mean[item] = ref + m1;
+    a.rstd[item] = 1.f / sqrtf(fmaxf(fmaf(-m1, m1, m2), 0.f) + a.eps);
   }
 }
 
@@ -650,7 +660,7 @@ __global__ void __launch_bounds__(TPI > 32 ? TPI : kNormThreads)
 // still in L2.
 template <int VEC, bool SILU>
 __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(NormArgs a, int lpr) {
-  const Tile t = make_tile<VEC>(a, lpr, gridDim.x - 1 - blockIdx.x);
+  const Tile t = make_tile<VEC>(a, lpr, 1, gridDim.x - 1 - blockIdx.x);
   if (!t.on) return;
   Vec<VEC> v[kNormRows];
 #pragma unroll
@@ -673,34 +683,33 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(NormArgs a, in
 
 // 1, backward: slot [channel] = (sum gz, sum gz h) of the part.
 template <int VEC, bool SILU>
-__global__ void __launch_bounds__(kNormThreads) norm_bwd_part_kernel(NormArgs a, int lpr, float2* __restrict__ slots) {
+__global__ void __launch_bounds__(kNormThreads)
+    norm_bwd_part_kernel(NormArgs a, int lpr, int per, float2* __restrict__ slots) {
   __shared__ float red[2 * VEC * kNormThreads];
-  const Tile t = make_tile<VEC>(a, lpr, blockIdx.x);
-  Vec<VEC> v[kNormRows], g[kNormRows];
-#pragma unroll
-  for (int i = 0; i < kNormRows; ++i) {
-    const int r = t.r0 + t.ty + i * t.nty;
-    v[i] = Vec<VEC>{};
-    g[i] = Vec<VEC>{};
-    if (t.on && r < t.r1) {
-      v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
-      g[i] = load_vec<VEC>(a.grad_y + r * a.gy_stride + t.col);
-    }
-  }
+  const Tile t = make_tile<VEC>(a, lpr, per, blockIdx.x);
   Columns<VEC> c{};
   if (t.on) c.load_params(a, t.col);
   for_parts(a, t.r0, t.r1, [&](int s, int lo, int hi) {
     Vec<VEC> s1{}, s2{};
     if (t.on) {
       c.load_stats(a, t.col, s);
+      for (int base = lo + t.ty; base < hi; base += t.nty * kNormRows) {
+        Vec<VEC> v[kNormRows], g[kNormRows];
 #pragma unroll
-      for (int i = 0; i < kNormRows; ++i) {
-        const int r = t.r0 + t.ty + i * t.nty;
-        if (r >= lo && r < hi) {
-          const Vec<VEC> h = c.normalised(v[i]), gz = activate_grad<SILU>(fma(c.gamma, h, c.beta), g[i]);
-          s1 = s1 + gz;
-          s2 = fma(gz, h, s2);
+        for (int i = 0; i < kNormRows; ++i) {
+          const int r = base + i * t.nty;
+          if (r < hi) {
+            v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
+            g[i] = load_vec<VEC>(a.grad_y + r * a.gy_stride + t.col);
+          }
         }
+#pragma unroll
+        for (int i = 0; i < kNormRows; ++i)
+          if (base + i * t.nty < hi) {
+            const Vec<VEC> h = c.normalised(v[i]), gz = activate_grad<SILU>(fma(c.gamma, h, c.beta), g[i]);
+            s1 = s1 + gz;
+            s2 = fma(gz, h, s2);
+          }
       }
     }
     float sum[2 * VEC];
@@ -722,7 +731,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_bwd_part_kernel(NormArgs a,
 template <int VEC, bool SILU>
 __global__ void __launch_bounds__(kNormThreads)
     norm_bwd_apply_kernel(NormArgs a, int lpr, const float2* __restrict__ terms) {
-  const Tile t = make_tile<VEC>(a, lpr, gridDim.x - 1 - blockIdx.x);
+  const Tile t = make_tile<VEC>(a, lpr, 1, gridDim.x - 1 - blockIdx.x);
   if (!t.on) return;
   Vec<VEC> v[kNormRows], g[kNormRows];
 #pragma unroll
@@ -889,6 +898,13 @@ cudaError_t launch_cluster(void (*kernel)(P...), const NormArgs& a, const Slabs&
   return cudaLaunchKernelEx(&cfg, kernel, a, f, args...);
 }
 
+// Rows of a tile of step 1, as a multiple of a block's registers: some four
+// tiles an SM, so that few slots have to be joined.
+int part_rows(const NormArgs& a, int rows, unsigned columns) {
+  const long long blocks = tiles_of(a.n, rows) * columns, per = (blocks + 4 * kFewBlocks - 1) / (4 * kFewBlocks);
+  return (int)(per < 1 ? 1 : per > 64 ? 64 : per);
+}
+
 template <bool BWD>
 cudaError_t join(const NormArgs& a, int rows, const float2* slots, float2* terms, cudaStream_t stream) {
   const long long items = (long long)a.samples * a.groups;
@@ -908,15 +924,17 @@ cudaError_t norm_fwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t str
     return f.rows == 4 ? launch_cluster(norm_fused_kernel<VEC, SILU, 4>, a, f, stream)
                        : launch_cluster(norm_fused_kernel<VEC, SILU, 8>, a, f, stream);
   const int lpr = lanes_per_row(a.channels, VEC), rows = rows_per_tile(a.channels, VEC);
-  const dim3 grid((unsigned)tiles_of(a.n, rows), (unsigned)((a.channels + lpr * VEC - 1) / (lpr * VEC)));
+  const unsigned columns = (unsigned)((a.channels + lpr * VEC - 1) / (lpr * VEC));
+  const int per = part_rows(a, rows, columns);
   cudaError_t e = cudaSuccess;
   if (a.n > 0) {
-    norm_part_kernel<VEC><<<grid, kNormThreads, 0, stream>>>(a, lpr, (float2*)ws);
+    norm_part_kernel<VEC><<<dim3((unsigned)tiles_of(a.n, per * rows), columns), kNormThreads, 0, stream>>>(a, lpr, per,
+                                                                                                          (float2*)ws);
     e = cudaGetLastError();
   }
-  if (e == cudaSuccess) e = join<false>(a, rows, (float2*)ws, nullptr, stream);
+  if (e == cudaSuccess) e = join<false>(a, per * rows, (float2*)ws, nullptr, stream);
   if (e == cudaSuccess && a.n > 0) {
-    norm_apply_kernel<VEC, SILU><<<grid, kNormThreads, 0, stream>>>(a, lpr);
+    norm_apply_kernel<VEC, SILU><<<dim3((unsigned)tiles_of(a.n, rows), columns), kNormThreads, 0, stream>>>(a, lpr);
     e = cudaGetLastError();
   }
   return e;
@@ -938,17 +956,19 @@ cudaError_t norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t str
     return e != cudaSuccess ? e : sum_params(a, (long long)a.samples * f.blocks, slots, sums, stream);
   }
   const int lpr = lanes_per_row(a.channels, VEC), rows = rows_per_tile(a.channels, VEC);
-  const long long tiles = tiles_of(a.n, rows), n_slots = tiles + a.samples;
-  const dim3 grid((unsigned)tiles, (unsigned)((a.channels + lpr * VEC - 1) / (lpr * VEC)));
+  const unsigned columns = (unsigned)((a.channels + lpr * VEC - 1) / (lpr * VEC));
+  const int per = part_rows(a, rows, columns);
+  const long long tiles = tiles_of(a.n, per * rows), n_slots = tiles + a.samples;
   cudaError_t e = cudaMemsetAsync(slots, 0, sizeof(float2) * (size_t)n_slots * a.channels, stream);
   if (e == cudaSuccess && a.n > 0) {
-    norm_bwd_part_kernel<VEC, SILU><<<grid, kNormThreads, 0, stream>>>(a, lpr, slots);
+    norm_bwd_part_kernel<VEC, SILU><<<dim3((unsigned)tiles, columns), kNormThreads, 0, stream>>>(a, lpr, per, slots);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && a.grad_x != nullptr && a.samples > 0) {
-    e = join<true>(a, rows, slots, terms, stream);
+    e = join<true>(a, per * rows, slots, terms, stream);
     if (e == cudaSuccess && a.n > 0) {
-      norm_bwd_apply_kernel<VEC, SILU><<<grid, kNormThreads, 0, stream>>>(a, lpr, terms);
+      norm_bwd_apply_kernel<VEC, SILU>
+          <<<dim3((unsigned)tiles_of(a.n, rows), columns), kNormThreads, 0, stream>>>(a, lpr, terms);
       e = cudaGetLastError();
     }
   }
