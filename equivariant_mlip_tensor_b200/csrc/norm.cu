@@ -536,6 +536,7 @@ __device__ __forceinline__ Tile make_tile(const NormArgs& a, int lpr, int per, i
 // 1, forward: slot [channel] = (mean, sum of squared deviations) of the part.
 template <int VEC>
 __global__ void __launch_bounds__(kNormThreads) norm_part_kernel(NormArgs a, int lpr, int per, float2* __restrict__ slots) {
+  grid_dependents_launch();
   __shared__ float red[VEC * kNormThreads];
   __shared__ float mean_of[VEC * 32];
   const Tile t = make_tile<VEC>(a, lpr, per, blockIdx.x);
@@ -615,6 +616,8 @@ constexpr int kJoinThreads = 1024;
 template <int TPI, bool BWD>
 __global__ void __launch_bounds__(TPI > 32 ? TPI : kNormThreads)
     norm_join_kernel(NormArgs a, int rows_per_tile, const float2* __restrict__ slots, float2* __restrict__ terms) {
+  grid_dependents_launch();
+  grid_dependency_wait();
   __shared__ float red[kJoinThreads / 32];
   const long long item = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / TPI;
   if (item >= (long long)a.samples * a.groups) return;  // whole items leave together
@@ -657,7 +660,8 @@ __global__ void __launch_bounds__(TPI > 32 ? TPI : kNormThreads)
 }
 
 // 3, forward.  The tiles from the last to the first: what step 1 read last is
-// still in L2.
+// still in L2.  The rows, which no launch of this call writes, are read before
+// the wait for step 2.
 template <int VEC, bool SILU>
 __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(NormArgs a, int lpr) {
   const Tile t = make_tile<VEC>(a, lpr, 1, gridDim.x - 1 - blockIdx.x);
@@ -670,6 +674,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(NormArgs a, in
   }
   Columns<VEC> c;
   c.load_params(a, t.col);
+  grid_dependency_wait();
   for_parts(a, t.r0, t.r1, [&](int s, int lo, int hi) {
     c.load_stats(a, t.col, s);
 #pragma unroll
@@ -685,6 +690,7 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(NormArgs a, in
 template <int VEC, bool SILU>
 __global__ void __launch_bounds__(kNormThreads)
     norm_bwd_part_kernel(NormArgs a, int lpr, int per, float2* __restrict__ slots) {
+  grid_dependents_launch();
   __shared__ float red[2 * VEC * kNormThreads];
   const Tile t = make_tile<VEC>(a, lpr, per, blockIdx.x);
   Columns<VEC> c{};
@@ -744,6 +750,8 @@ __global__ void __launch_bounds__(kNormThreads)
   }
   Columns<VEC> c;
   c.load_params(a, t.col);
+  grid_dependents_launch();
+  grid_dependency_wait();
   for_parts(a, t.r0, t.r1, [&](int s, int lo, int hi) {
     c.load_stats(a, t.col, s);
     Vec<VEC> m1, m2;
@@ -828,19 +836,20 @@ bool vec4_rows(const void* p, long long stride) { return stride % 4 == 0 && ((ui
 
 // The fused split for these sizes, or count = 0 for the tiles.  Measured on
 // fp32 rows with SiLU, forward / backward in microseconds:
-//   256 samples x 30 rows x 128 channels: whole rows, 256 threads, 4 rows each 8.5 / 10.4
-//     (tiles 25 / 33);
-//   61 samples, 131 101 rows x 256: 64-byte slabs 87 / 135, 32-byte ones 142 / 174 (tiles 108 / 187);
-//   2 000 samples, 130 000 rows x 256: whole rows 98 / 139, 64-byte slabs over 200 (tiles 160 / 255);
-//   1 sample of 20 000 rows x 128: 64-byte slabs, 8 blocks of 512 threads 16.6 / 23 (tiles 18.7 / 32);
-//   1 sample of 130 000 rows x 256: that split 106 / 163, the tiles 93 / 157.
+//   256 samples x 30 rows x 128 channels: whole rows, 256 threads, 4 rows each 7 / 8 (tiles 20 / 26);
+//   254 samples, 130 000 rows x 256: 128-byte slabs 88 / 119 (whole rows 119 / 150, tiles 96 / 157);
+//   4 000 samples, 130 000 rows x 256: whole rows, 128 threads 137 / 144, 256 threads 189 / 175 (tiles 255 / 347);
+//   61 samples, 131 101 rows x 256: 64-byte slabs 104 / 154, the tiles 86 / 145;
+//   1 sample of 130 000 rows x 256: a cluster of 8 per 64-byte slab 88 / 150, the tiles 78 / 126;
+//   1 sample of 20 000 rows x 128: a cluster of 8 per 64-byte slab 15 / 20, the tiles 14 / 23 in five launches.
 // So slabs narrow, down to 64 bytes a row, while the usual sample does not fit
 // the registers and there are not yet many blocks; then few blocks become a
-// cluster of larger ones; and a longest sample that would keep its blocks
-// reading long after the others goes to the tiles.
+// cluster of larger ones.  Long samples of a tensor that leaves L2 go to the
+// tiles, which read whole rows, as do longest samples that would keep their
+// blocks reading long after the others.
 constexpr long long kFewBlocks = 148, kManyBlocks = 8 * kFewBlocks;
 template <int VEC>
-Slabs fused_slabs(const NormArgs& a, int max_rows, bool backward) {
+Slabs fused_slabs(const NormArgs& a, int max_rows) {
   Slabs f{};
   const int cpg = a.channels / a.groups;
   const int most = VEC == 4 ? kSlabColumns : 32;  // 32 lanes across
@@ -854,6 +863,7 @@ Slabs fused_slabs(const NormArgs& a, int max_rows, bool backward) {
   long long longest = max_rows > 0 ? max_rows : a.samples == 1 ? a.n : 4 * average + 64;
   if (longest > a.n) longest = a.n;
   const long long usual = longest < 2 * average ? longest : 2 * average;
+  if (average > 1024 && (long long)a.n * a.channels > (16 << 20)) return f;
   auto set = [&](int groups) {
     f.groups = groups < a.groups ? groups : a.groups;
     f.count = (a.groups + f.groups - 1) / f.groups;
@@ -873,9 +883,8 @@ Slabs fused_slabs(const NormArgs& a, int max_rows, bool backward) {
   while (f.blocks < 8 && held() * f.blocks < longest && blocks() * f.blocks < kFewBlocks) f.blocks *= 2;
   if (blocks() * f.blocks <= kFewBlocks && held() * f.blocks < longest) f.threads = kFusedMost;
   if (f.blocks == 1) {
-    // small samples: fewer rows in registers, then fewer threads.  Many blocks: more of them a SM
-    // (the forward only: the backward would compute its rows twice as often)
-    if (held() / 2 >= usual || (!backward && blocks() >= kManyBlocks)) f.rows = 4;
+    if (blocks() >= kManyBlocks) f.threads = 128;  // small blocks overlap better
+    if (held() / 2 >= usual) f.rows = 4;  // small samples
     while (f.threads > 128 && held() / 2 >= usual) f.threads /= 2;
   }
   if (held() * f.blocks * (blocks() < 4 * kFewBlocks ? 8 : 32) < longest || blocks() * f.blocks > 0x7fffffffLL) f.count = 0;
@@ -909,17 +918,19 @@ template <bool BWD>
 cudaError_t join(const NormArgs& a, int rows, const float2* slots, float2* terms, cudaStream_t stream) {
   const long long items = (long long)a.samples * a.groups;
   // a warp per item while a sample has few slots; a block for long samples
+  // (launched dependent on step 1: each waits for it before its first read)
   const bool wide = ((double)a.n / a.samples / rows + 1) * (a.channels / a.groups) > 512;
   const long long blocks = wide ? items : (items * 32 + kNormThreads - 1) / kNormThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  if (wide) norm_join_kernel<kJoinThreads, BWD><<<(unsigned)blocks, kJoinThreads, 0, stream>>>(a, rows, slots, terms);
-  else norm_join_kernel<32, BWD><<<(unsigned)blocks, kNormThreads, 0, stream>>>(a, rows, slots, terms);
-  return cudaGetLastError();
+  return wide ? launch_kernel(norm_join_kernel<kJoinThreads, BWD>, dim3((unsigned)blocks), dim3(kJoinThreads), 0, stream,
+                              a.n > 0, a, rows, slots, terms)
+              : launch_kernel(norm_join_kernel<32, BWD>, dim3((unsigned)blocks), dim3(kNormThreads), 0, stream,
+                              a.n > 0, a, rows, slots, terms);
 }
 
 template <int VEC, bool SILU>
 cudaError_t norm_fwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t stream) {
-  const Slabs f = fused_slabs<VEC>(a, max_rows, false);
+  const Slabs f = fused_slabs<VEC>(a, max_rows);
   if (f.count > 0)
     return f.rows == 4 ? launch_cluster(norm_fused_kernel<VEC, SILU, 4>, a, f, stream)
                        : launch_cluster(norm_fused_kernel<VEC, SILU, 8>, a, f, stream);
@@ -933,10 +944,9 @@ cudaError_t norm_fwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t str
     e = cudaGetLastError();
   }
   if (e == cudaSuccess) e = join<false>(a, per * rows, (float2*)ws, nullptr, stream);
-  if (e == cudaSuccess && a.n > 0) {
-    norm_apply_kernel<VEC, SILU><<<dim3((unsigned)tiles_of(a.n, rows), columns), kNormThreads, 0, stream>>>(a, lpr);
-    e = cudaGetLastError();
-  }
+  if (e == cudaSuccess && a.n > 0)
+    e = launch_kernel(norm_apply_kernel<VEC, SILU>, dim3((unsigned)tiles_of(a.n, rows), columns), dim3(kNormThreads), 0,
+                      stream, true, a, lpr);
   return e;
 }
 
@@ -949,7 +959,7 @@ cudaError_t norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t str
   float2* terms = (float2*)ws;
   float2* sums = (float2*)((char*)ws + terms_bytes(a));
   float2* slots = (float2*)((char*)ws + terms_bytes(a) + sums_bytes(a));
-  const Slabs f = fused_slabs<VEC>(a, max_rows, true);
+  const Slabs f = fused_slabs<VEC>(a, max_rows);
   if (f.count > 0) {
     const cudaError_t e = f.rows == 4 ? launch_cluster(norm_bwd_fused_kernel<VEC, SILU, 4>, a, f, stream, slots)
                                       : launch_cluster(norm_bwd_fused_kernel<VEC, SILU, 8>, a, f, stream, slots);
@@ -966,11 +976,9 @@ cudaError_t norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t str
   }
   if (e == cudaSuccess && a.grad_x != nullptr && a.samples > 0) {
     e = join<true>(a, per * rows, slots, terms, stream);
-    if (e == cudaSuccess && a.n > 0) {
-      norm_bwd_apply_kernel<VEC, SILU>
-          <<<dim3((unsigned)tiles_of(a.n, rows), columns), kNormThreads, 0, stream>>>(a, lpr, terms);
-      e = cudaGetLastError();
-    }
+    if (e == cudaSuccess && a.n > 0)
+      e = launch_kernel(norm_bwd_apply_kernel<VEC, SILU>, dim3((unsigned)tiles_of(a.n, rows), columns),
+                        dim3(kNormThreads), 0, stream, true, a, lpr, (const float2*)terms);
   }
   return e != cudaSuccess ? e : sum_params(a, n_slots, slots, sums, stream);
 }
@@ -984,8 +992,8 @@ size_t norm_workspace(int n, int samples, int channels, int groups, int max_rows
   a.samples = samples;
   a.channels = channels;
   a.groups = groups;
-  const Slabs one = fused_slabs<1>(a, max_rows, backward);
-  const Slabs four = channels % 4 == 0 ? fused_slabs<4>(a, max_rows, backward) : one;
+  const Slabs one = fused_slabs<1>(a, max_rows);
+  const Slabs four = channels % 4 == 0 ? fused_slabs<4>(a, max_rows) : one;
   const bool fused = one.count > 0 && four.count > 0;
   if (fused && !backward) return 0;
   const int blocks = one.blocks > four.blocks ? one.blocks : four.blocks;
