@@ -333,7 +333,7 @@ constexpr int kEmbedUnroll = 8;
 // found by a search of the sorted tokens; in the others, one worker takes one
 // (chunk, column slice).
 template <int VEC>
-__global__ void __launch_bounds__(kEmbedThreads) embed_bwd_kernel(EmbedBwdArgs a, int clear_blocks) {
+__global__ void __launch_bounds__(kEmbedThreads, 4) embed_bwd_kernel(EmbedBwdArgs a, int clear_blocks) {
   grid_dependents_launch();
   const int lane = threadIdx.x & (a.lpr - 1);
   if ((int)blockIdx.x < clear_blocks) {
