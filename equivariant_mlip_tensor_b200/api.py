@@ -314,7 +314,7 @@ def _norm_shape(x, gamma, beta, groups, graph_ptr, activation):
     _check(graph_ptr, torch.int32, "graph_ptr")
     if activation not in ACTIVATIONS:
         raise ValueError(f"activation must be one of {list(ACTIVATIONS)}, got {activation!r}")
-    if groups < 1 or c % groups:
+    if groups < 1 or c < 1 or c % groups:
         raise ValueError(f"{c} channels cannot be cut into {groups} equal groups")
     if graph_ptr is not None and graph_ptr.numel() < 1:
         raise ValueError("graph_ptr must hold n_samples + 1 offsets")

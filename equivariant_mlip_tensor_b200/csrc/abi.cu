@@ -1125,10 +1125,10 @@ cgtp_status cgtp_embed_backward(int n, int n_rows, int width, const int* order, 
 
 cgtp_status cgtp_group_norm_workspace_size(int n, int n_samples, int channels, int groups, int max_rows, int backward,
                                            size_t* bytes) {
-  if (n < 0 || n > kMaxTokens || n_samples < 0 || channels < 0 || groups < 1 || channels % groups != 0 ||
+  if (n < 0 || n > kMaxTokens || n_samples < 0 || channels < 1 || groups < 1 || channels % groups != 0 ||
       max_rows < 0 || bytes == nullptr)
     return CGTP_ERR_INVALID_ARG;
-  *bytes = channels == 0 ? 0 : norm_workspace(n, n_samples, channels, groups, max_rows, backward != 0);
+  *bytes = norm_workspace(n, n_samples, channels, groups, max_rows, backward != 0);
   return CGTP_OK;
 }
 
@@ -1139,7 +1139,7 @@ static cgtp_status norm_args(const NormArgs& a, int max_rows, bool backward, con
   if (a.act != CGTP_ACT_NONE && a.act != CGTP_ACT_SILU) return CGTP_ERR_INVALID_ARG;
   if (a.ptr == nullptr && a.samples != 1) return CGTP_ERR_INVALID_ARG;
   if (!rows_ok(a.x, a.n, a.channels, a.x_stride)) return CGTP_ERR_INVALID_ARG;
-  if (a.samples > 0 && a.channels > 0 && (a.mean == nullptr || a.rstd == nullptr)) return CGTP_ERR_INVALID_ARG;
+  if (a.samples > 0 && (a.mean == nullptr || a.rstd == nullptr)) return CGTP_ERR_INVALID_ARG;
   return workspace_ok(ws, ws_bytes, need);
 }
 

@@ -1007,14 +1007,13 @@ size_t norm_workspace(int n, int samples, int channels, int groups, int max_rows
 }
 
 cudaError_t launch_norm_fwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t stream) {
-  if (a.samples == 0 || a.channels == 0) return cudaSuccess;
+  if (a.samples == 0) return cudaSuccess;
   const bool v4 = a.channels % 4 == 0 && vec4_rows(a.x, a.x_stride) && vec4_rows(a.y, a.y_stride);
   if (v4) return a.act ? norm_fwd<4, true>(a, max_rows, ws, stream) : norm_fwd<4, false>(a, max_rows, ws, stream);
   return a.act ? norm_fwd<1, true>(a, max_rows, ws, stream) : norm_fwd<1, false>(a, max_rows, ws, stream);
 }
 
 cudaError_t launch_norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t stream) {
-  if (a.channels == 0) return cudaSuccess;
   const bool v4 = a.channels % 4 == 0 && vec4_rows(a.x, a.x_stride) && vec4_rows(a.grad_y, a.gy_stride) &&
                   (a.grad_x == nullptr || vec4_rows(a.grad_x, a.gx_stride));
   if (v4) return a.act ? norm_bwd<4, true>(a, max_rows, ws, stream) : norm_bwd<4, false>(a, max_rows, ws, stream);

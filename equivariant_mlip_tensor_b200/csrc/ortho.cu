@@ -48,7 +48,7 @@ constexpr double kNsEps = 1e-7;
 // A tensor-core accumulator rounds towards zero at every addition, so a large
 // diagonal term would come out too small by the same 2e-7 everywhere, and
 // a X + P X loses most of its leading digits when the values are near 1
-// (64 x 1920: 3.4e-6 of the result with the diagonals inside, FIXME without).
+// (64 x 1920: 3.4e-6 of the result with the diagonals inside, 5.5e-7 so).
 constexpr int kSmallThreads = 512;  // and one more warp, which issues the products
 constexpr int kSmallSide = 128;     // rows of X
 constexpr int kSmallColumns = 256;  // columns of X in one block
@@ -536,10 +536,15 @@ cudaError_t launch_small(int batch, int rows, int cols, int steps, float scale, 
 // operand.  The diagonal of X X^T, long sums of like signs, is summed in fp32 where
 // X is made.  The launches are dependent ones (programmatic stream serialization):
 // each sets up while the one before ends and waits for it before its first
-// access to global memory.  Four accumulators fill the tensor memory: one for low high + high
-// low, three that share the columns of high high, so that no entry is rounded
-// towards zero more often than once in 48 columns (2 x 1024 x 1024, one
-// accumulator for all but X X^T: 4.9e-6 of the result, with four: FIXME).
+// access to global memory.  Four accumulators fill the tensor memory: one for
+// low high + high low, three that share the columns of high high, so that an
+// accumulator is rounded towards zero a third as often (2 x 1024 x 1024: 1.7e-6
+// of the result, plain fp32 products 3.1e-6; with one accumulator 4.9e-6).
+// 2 x 1024 x 1024 takes 245 us, 15 products of 14 us after the set-up: 8 us the MMAs and their
+// loads (6.6 at the tensor rate of 128 blocks), 6 us from one launch's last
+// store to the next one's first product and the epilogue.  Measured and not kept: pairs of
+// blocks that share the right operand (cta_group::2, 283 us: the pair's barriers
+// cost more than the 25 % fewer bytes) and symmetric products computed by half (261 us).
 constexpr int kTileBytes = 128 * 128, kStages = 3, kStageBytes = 4 * kTileBytes;
 constexpr int kLargeThreads = kSmallThreads + 64;
 constexpr int kLargeParts = 3;

@@ -180,6 +180,28 @@ def test_nonfinite_values_stay_in_their_row(api):
     assert torch.isinf(grad[2, 0]) and grad[2, 1] == 1
 
 
+def test_offsets_beyond_32_bits(api):
+    """Rows 32 768 floats apart (the last starts at 2.3e9), as features, as the
+    gradient of features and as rows of the table."""
+    import torch
+    rng = np.random.default_rng(8)
+    n, rows, width, stride = 70000, 50, 8, 32768
+    tok = _tokens(rng, n, rows, "mixed")
+    table, gh = (rng.standard_normal(s).astype(np.float32) for s in ((rows, width), (n, width)))
+    wide = torch.empty((n, stride), device="cuda")
+    api.embed_forward(cuda(tok), cuda(table), out=wide[:, :width])
+    valid = (tok >= 0) & (tok < rows)
+    assert np.array_equal(host(wide[:, :width].contiguous()), np.where(valid[:, None], table[np.where(valid, tok, 0)], 0))
+    wide[:, :width].copy_(cuda(gh))
+    _check_backward(api.embed_backward(api.token_sort(cuda(tok), rows), wide[:, :width]), tok, rows, gh, 1.0)
+    few = torch.tensor([69999, 0, 69999], dtype=torch.int32, device="cuda")
+    out = api.embed_forward(few, wide)
+    assert torch.equal(out[0], wide[69999]) and torch.equal(out[1], wide[0])
+    grad = api.embed_backward(api.token_sort(few, n), out, out=wide)  # the table's own storage
+    assert torch.equal(grad[69999], out[0] + out[2]) and torch.equal(grad[0], out[1])
+    assert not grad[1:69999].any()
+
+
 def test_streams_and_graph_replay(api):
     """On another stream than the default one, and captured once, replayed on new inputs."""
     import torch

@@ -108,6 +108,34 @@ def test_both_directions_match_the_oracle(api, n, samples, c, groups, kind, acti
     assert rel_err(host(gb), wb) <= GRAD_TOL
 
 
+LARGE = [(20000, 1, 128, 32, None), (9000, 2, 64, 4, "ragged"), (100003, 5, 260, 1, "ragged"), (60000, 700, 140, 1, "ragged"),
+         (20000, 3, 70, 2, "ragged"), (131072, 1, 128, 4, None), (30000, 3000, 32, 4, "ragged"), (50000, 40, 36, 1, "inner")]
+
+
+@pytest.mark.parametrize("n,samples,c,groups,kind", LARGE)
+@pytest.mark.parametrize("hint", [0, 1])
+def test_long_samples_and_many_samples(api, n, samples, c, groups, kind, hint):
+    """Rows beyond a block's registers, clusters, tiles of several register
+    loads, samples that end inside a tile.  A value passes through more roundings in a row
+    than at the sizes above: up to 8 register loads of 8 rows with a join each
+    (5 operations), 64 slots a thread and the trees, 256 in all, so the bound grows by
+    256 / K."""
+    rng = np.random.default_rng(n + c)
+    ptr = _ptr(rng, n, samples, kind)
+    x = (rng.standard_normal((n, c)) * (0.5 + rng.random(c)) + rng.standard_normal(c)).astype(np.float32)
+    gamma, beta = (1 + 0.3 * rng.standard_normal(c)).astype(np.float32), rng.standard_normal(c).astype(np.float32)
+    gy = rng.standard_normal((n, c)).astype(np.float32)
+    longest = n if ptr is None else int(np.diff(ptr).max())
+    kw = dict(graph_ptr=_i32(ptr), activation="silu", max_rows=longest if hint else 0)
+    y, mean, rstd = api.group_norm_forward(cuda(x), cuda(gamma), cuda(beta), groups, eps=EPS, **kw)
+    want, om, orstd, bound = _forward_bound(x, gamma, beta, groups, ptr, "silu")
+    m = _inside(ptr, n)
+    assert (np.abs(host(y) - want)[m] <= (256 / K * bound)[m]).all()
+    gx, gg, gb = api.group_norm_backward(cuda(x), cuda(gamma), cuda(beta), groups, mean, rstd, cuda(gy), **kw)
+    wx, wg, wb = onorm.backward(x, gamma, beta, groups, ptr, EPS, "silu", gy)
+    assert rel_err(host(gx)[m], wx[m]) <= GRAD_TOL and rel_err(host(gg), wg) <= GRAD_TOL and rel_err(host(gb), wb) <= GRAD_TOL
+
+
 @pytest.mark.parametrize("width", [16, 10])
 @pytest.mark.parametrize("hint", [0, 40])
 def test_scalar_block_in_place_and_rows_left_alone(api, width, hint):
@@ -251,6 +279,27 @@ def test_streams_graph_replay_and_equal_bits(api, hint):
                 assert torch.equal(a, b)
 
 
+def test_row_offsets_beyond_32_bits(api):
+    """70 000 rows, 32 768 floats apart: the last one starts at 2.3e9 floats."""
+    import torch
+    rng = np.random.default_rng(17)
+    n, c, groups, stride = 70000, 8, 2, 32768
+    xh, gh = (rng.standard_normal((n, c)).astype(np.float32) for _ in range(2))
+    x, g = (torch.empty((n, stride), device="cuda")[:, :c] for _ in range(2))
+    x.copy_(cuda(xh))
+    g.copy_(cuda(gh))
+    ptr = [0, 69990, n]
+    for hint in (0, n):
+        y, mean, rstd = api.group_norm_forward(x, None, None, groups, graph_ptr=_i32(ptr), activation="silu", max_rows=hint)
+        gx, gg, gb = api.group_norm_backward(x, None, None, groups, mean, rstd, g, graph_ptr=_i32(ptr), activation="silu",
+                                             max_rows=hint, grad_x=g if hint else None)
+        want = onorm.forward(xh, None, None, groups, ptr, EPS, "silu")[0]
+        wx, wg, wb = onorm.backward(xh, None, None, groups, ptr, EPS, "silu", gh)
+        # sums of 280 000 values: in runs of a few hundred (tiles, chunks of registers) joined by trees
+        assert rel_err(host(y), want) <= 4 * K * U
+        assert rel_err(host(gx), wx) <= GRAD_TOL and rel_err(host(gg), wg) <= GRAD_TOL and rel_err(host(gb), wb) <= GRAD_TOL
+
+
 def test_requested_outputs_alone_and_empty(api):
     import torch
     rng = np.random.default_rng(16)
@@ -275,7 +324,7 @@ def test_refusals(api):
     x = torch.zeros((6, 8), device="cuda")
     v = torch.zeros(8, device="cuda")
     s = torch.zeros((1, 2), device="cuda")
-    for bad in (lambda: api.group_norm_forward(x, v, v, 3), lambda: api.group_norm_forward(x, v, v, 0),
+    for bad in (lambda: api.group_norm_forward(x[:, :0], None, None, 1), lambda: api.group_norm_forward(x, v, v, 3), lambda: api.group_norm_forward(x, v, v, 0),
                 lambda: api.group_norm_forward(x.half(), v, v, 2), lambda: api.group_norm_forward(x.cpu(), v, v, 2),
                 lambda: api.group_norm_forward(x, v[:4], v, 2), lambda: api.group_norm_forward(x.t(), None, None, 2),
                 lambda: api.group_norm_forward(x, v, v, 2, activation="relu"),

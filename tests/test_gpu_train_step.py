@@ -187,3 +187,37 @@ def test_two_streams_at_once(api):
         torch.cuda.synchronize()
         for a, b in zip(got, want):
             assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+FIRST_CALLS = """
+import torch
+from equivariant_mlip_tensor_b200 import api
+s = torch.cuda.Stream()
+tok = torch.arange(20000, dtype=torch.int32, device="cuda") % 7
+g = torch.ones((20000, 8), device="cuda")
+m = [torch.randn(2, *k, device="cuda") for k in ((8, 8), (16, 600), (150, 160))]
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph, stream=s):
+    x = api.embed_forward(tok, g[:7])
+    t = api.embed_backward(api.token_sort(tok, 7), g)
+    few = api.embed_backward(api.token_sort(tok[:500].contiguous(), 7), g[:500])
+    y, mean, rstd = api.group_norm_forward(g, None, None, 2, activation="silu")
+    b = api.group_norm_backward(g, None, None, 2, mean, rstd, x, activation="silu")
+    o = [api.orthogonalise(k) for k in m]
+graph.replay()
+torch.cuda.synchronize()
+want = torch.bincount(tok.long()).float()[:, None].expand(7, 8)
+assert torch.equal(t, want) and torch.equal(x, g) and not y.any() and all(torch.isfinite(k).all() for k in o)
+assert torch.equal(few.sum(0), torch.full((8,), 500.0, device="cuda"))
+print("captured")
+"""
+
+
+def test_first_call_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]

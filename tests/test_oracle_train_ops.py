@@ -80,6 +80,8 @@ def test_host_errors():
     assert L.cgtp_embed_backward_workspace_size(4, -1, ctypes.byref(sz)) == 1
     assert L.cgtp_group_norm_workspace_size(4, 1, 12, 5, 0, 0, ctypes.byref(sz)) == 1   # 12 channels, 5 groups
     assert L.cgtp_group_norm_workspace_size(4, 1, 12, 0, 0, 0, ctypes.byref(sz)) == 1
+    assert L.cgtp_group_norm_workspace_size(4, 1, 0, 1, 0, 0, ctypes.byref(sz)) == 1
+    assert L.cgtp_group_norm_workspace_size(4, 1, 12, 4, -1, 0, ctypes.byref(sz)) == 1
     assert L.cgtp_orthogonalise_workspace_size(1, 8193, 4, ctypes.byref(sz)) == 1
     assert L.cgtp_orthogonalise_workspace_size(65536, 4, 4, ctypes.byref(sz)) == 1
     # token sort: missing and aliased arrays, workspace
