@@ -654,8 +654,9 @@ __global__ void __launch_bounds__(TPI > 32 ? TPI : kNormThreads)
   if constexpr (BWD) {
     terms[item] = make_float2(m1, m2);
   } else {
+    const float var = fmaf(-m1, m1, m2);
     a.mean[item] = ref + m1;
-    a.rstd[item] = 1.f / sqrtf(fmaxf(fmaf(-m1, m1, m2), 0.f) + a.eps);
+    a.rstd[item] = 1.f / sqrtf((var < 0.f ? 0.f : var) + a.eps);  // NaN stays
   }
 }
 
@@ -807,20 +808,23 @@ __global__ void __launch_bounds__(1024)
 }
 constexpr int kParamRows = 1024, kParamParts = 64;
 
-cudaError_t sum_params(const NormArgs& a, long long rows, const float2* slots, float2* sums, cudaStream_t stream) {
+// after_kernel: the launch before this one in the stream is a kernel of the same call.
+cudaError_t sum_params(const NormArgs& a, long long rows, const float2* slots, float2* sums, bool after_kernel,
+                       cudaStream_t stream) {
   if (a.grad_gamma == nullptr && a.grad_beta == nullptr) return cudaSuccess;
   const unsigned columns = (unsigned)((a.channels + 31) / 32);
   cudaError_t e = cudaSuccess;
   if (rows > kParamRows) {
     const int per = (int)((rows + kParamParts - 1) / kParamParts);
-    e = launch_kernel(norm_param_kernel, dim3(columns, kParamParts), dim3(1024), 0, stream, true, (int)rows, per,
-                      a.channels, slots, sums, (float*)nullptr, (float*)nullptr);
+    e = launch_kernel(norm_param_kernel, dim3(columns, kParamParts), dim3(1024), 0, stream, after_kernel,
+                      (int)rows, per, a.channels, slots, sums, (float*)nullptr, (float*)nullptr);
     if (e != cudaSuccess) return e;
     slots = sums;
     rows = kParamParts;
+    after_kernel = true;
   }
-  return launch_kernel(norm_param_kernel, dim3(columns), dim3(1024), 0, stream, true, (int)rows, (int)rows, a.channels,
-                       slots, (float2*)nullptr, a.grad_gamma, a.grad_beta);
+  return launch_kernel(norm_param_kernel, dim3(columns), dim3(1024), 0, stream, after_kernel, (int)rows, (int)rows,
+                       a.channels, slots, (float2*)nullptr, a.grad_gamma, a.grad_beta);
 }
 
 // ---------------------------------------------------------------- launching
@@ -963,7 +967,7 @@ cudaError_t norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t str
   if (f.count > 0) {
     const cudaError_t e = f.rows == 4 ? launch_cluster(norm_bwd_fused_kernel<VEC, SILU, 4>, a, f, stream, slots)
                                       : launch_cluster(norm_bwd_fused_kernel<VEC, SILU, 8>, a, f, stream, slots);
-    return e != cudaSuccess ? e : sum_params(a, (long long)a.samples * f.blocks, slots, sums, stream);
+    return e != cudaSuccess ? e : sum_params(a, (long long)a.samples * f.blocks, slots, sums, true, stream);
   }
   const int lpr = lanes_per_row(a.channels, VEC), rows = rows_per_tile(a.channels, VEC);
   const unsigned columns = (unsigned)((a.channels + lpr * VEC - 1) / (lpr * VEC));
@@ -980,7 +984,7 @@ cudaError_t norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t str
       e = launch_kernel(norm_bwd_apply_kernel<VEC, SILU>, dim3((unsigned)tiles_of(a.n, rows), columns),
                         dim3(kNormThreads), 0, stream, true, a, lpr, (const float2*)terms);
   }
-  return e != cudaSuccess ? e : sum_params(a, n_slots, slots, sums, stream);
+  return e != cudaSuccess ? e : sum_params(a, n_slots, slots, sums, a.n > 0, stream);
 }
 
 }  // namespace

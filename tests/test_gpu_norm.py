@@ -219,6 +219,19 @@ def test_nonfinite_values_stay_in_their_graph_and_group(api, hint):
     assert np.isnan(host(gb)[0]) and np.isfinite(host(gb)[1:]).all()
 
 
+def test_infinite_value_leaves_no_number_in_its_group_of_a_long_sample(api):
+    """Enough rows for the split by tiles: the variance of a group that holds an
+    infinity is no number, and so are its rstd and every result."""
+    rng = np.random.default_rng(8)
+    n, c = 140000, 128
+    ptr = np.array([0, n // 2, n])
+    x = rng.standard_normal((n, c)).astype(np.float32)
+    x[n // 2 + 4321, 70] = np.inf
+    y, mean, rstd = api.group_norm_forward(cuda(x), None, None, 2, graph_ptr=_i32(ptr))
+    assert np.isnan(host(rstd)[1, 1]) and np.isfinite(host(rstd)).sum() == 3
+    assert np.isnan(host(y)[n // 2:, 64:]).all() and np.isfinite(host(y)).sum() == n * c - n // 2 * 64
+
+
 def test_gradient_against_differences(api):
     """Directional differences of the kernel's own forward.
 
