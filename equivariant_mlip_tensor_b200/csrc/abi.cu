@@ -1125,7 +1125,7 @@ cgtp_status cgtp_embed_backward(int n, int n_rows, int width, const int* order, 
 
 cgtp_status cgtp_group_norm_workspace_size(int n, int n_samples, int channels, int groups, int max_rows, int backward,
                                            size_t* bytes) {
-  if (n < 0 || n > kMaxTokens || n_samples < 0 || channels < 1 || groups < 1 || channels % groups != 0 ||
+  if (n < 0 || n > kMaxTokens || n_samples < 0 || n_samples > kMaxTokens || channels < 1 || groups < 1 || channels % groups != 0 ||
       max_rows < 0 || bytes == nullptr)
     return CGTP_ERR_INVALID_ARG;
   *bytes = norm_workspace(n, n_samples, channels, groups, max_rows, backward != 0);

@@ -176,46 +176,57 @@ struct Columns {
 };
 
 // ------------------------------------------------------------------- fused
-struct Slabs {
-  int lanes;    // threads across a slab's columns (a power of two, at most 32)
-  int groups;   // whole groups of a slab
-  int count;    // slabs
-  int blocks;   // blocks per sample and slab (a cluster)
-  int threads;  // of a block
-  int rows;     // rows per thread, held in registers
-};
 constexpr int kSlabColumns = 128;
+struct Slabs {
+  int lanes;        // threads across a slab's columns (a power of two, at most 32)
+  int groups;       // whole groups of a slab
+  int count;        // slabs
+  int blocks;       // blocks per sample and slab (a cluster): 1 << shift
+  int threads;      // of a block
+  int rows;         // rows per thread, held in registers
+  int shift;
+  unsigned per_cpg; // 2^20 / channels per group, rounded up
+  int team;         // threads that sum one group (a power of two, at most 32)
+};
+// x / (channels per group), x < 16 * 128: the product is over by less than 2^11 of 2^20, a step is 2^13 at least
+__device__ __forceinline__ int group_of(const Slabs& f, int x) { return (int)((unsigned)x * f.per_cpg >> 20); }
 
 // What the threads of a block share: column sums by warp, then by column or by group.
 struct FusedShared {
   float red[2][kFusedMost / 32][kSlabColumns];
   float col[2][kSlabColumns];
   float sum[2][kSlabColumns];    // by group: this block's
-  float total[2][kSlabColumns];  // by group: the cluster's
+  float total[2][kSlabColumns];  // by group: the results that every block of the cluster has
 };
 
 struct Place {
-  int sample, part, lane, ty, nty, c0, columns, groups, col, r0, r1, rows;
+  int sample, part, lane, ty, nty, c0, columns, groups, cpg, g0, col, r0, r1, rows;
   bool on;
 };
 template <int VEC>
 __device__ __forceinline__ Place place_of(const NormArgs& a, const Slabs& f) {
   Place p;
-  p.part = blockIdx.x % f.blocks;
-  const int slab = blockIdx.x / f.blocks % f.count, cpg = a.channels / a.groups;
-  p.sample = blockIdx.x / f.blocks / f.count;
+  p.part = blockIdx.x & (f.blocks - 1);
+  p.sample = blockIdx.x >> f.shift;
+  int slab = 0;
+  if (f.count > 1) {
+    slab = p.sample % f.count;
+    p.sample /= f.count;
+  }
+  p.cpg = a.channels / a.groups;
   p.lane = threadIdx.x & (f.lanes - 1);
   p.ty = threadIdx.x / f.lanes;
   p.nty = blockDim.x / f.lanes;
-  p.groups = min(f.groups, a.groups - slab * f.groups);
-  p.c0 = slab * f.groups * cpg;
-  p.columns = p.groups * cpg;
+  p.g0 = slab * f.groups;
+  p.groups = min(f.groups, a.groups - p.g0);
+  p.c0 = p.g0 * p.cpg;
+  p.columns = p.groups * p.cpg;
   p.col = p.c0 + p.lane * VEC;
   p.on = p.lane * VEC < p.columns;
   const int2 b = sample_rows(a, p.sample);
   p.rows = b.y - b.x;
-  p.r0 = b.x + (int)((long long)p.rows * p.part / f.blocks);
-  p.r1 = b.x + (int)((long long)p.rows * (p.part + 1) / f.blocks);
+  p.r0 = b.x + (int)((long long)p.rows * p.part >> f.shift);
+  p.r1 = b.x + (int)((long long)p.rows * (p.part + 1) >> f.shift);
   return p;
 }
 
@@ -226,33 +237,43 @@ __device__ __forceinline__ void sum_rows(Vec<VEC> v, const Place& p, int lanes, 
   for (int o = lanes; o < 32; o <<= 1)
 #pragma unroll
     for (int j = 0; j < VEC; ++j) v.v[j] += __shfl_xor_sync(0xffffffffu, v.v[j], o);
-  if ((threadIdx.x & 31) < lanes)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j)
-      if (p.lane * VEC + j < kSlabColumns) red[threadIdx.x >> 5][p.lane * VEC + j] = v.v[j];
+  if ((threadIdx.x & 31) < lanes && p.lane * VEC < kSlabColumns) store_vec<VEC>(&red[threadIdx.x >> 5][p.lane * VEC], v);
 }
 
-// Group sums over the columns (and warps) of red, then over the cluster, into total.
-__device__ __forceinline__ void sum_groups(const Place& p, int cpg, int blocks, const float (*red)[kSlabColumns],
-                                           float* sum, float* total) {
-  __syncthreads();
-  for (int g = threadIdx.x >> 5; g < p.groups; g += blockDim.x >> 5) {
+// For each group of the slab, value(g, e) summed over e < count by a team of
+// threads, in a fixed order; last(g, sum) on one thread.
+template <class V, class L>
+__device__ __forceinline__ void team_sums(const Place& p, int team, int count, V&& value, L&& last) {
+  const int mine = threadIdx.x & (team - 1), teams = blockDim.x / team;
+  for (int g0 = 0; g0 < p.groups; g0 += teams) {  // the same for every thread
+    const int g = g0 + threadIdx.x / team;
     float s = 0.f;
-    for (int e = threadIdx.x & 31; e < (int)(blockDim.x >> 5) * cpg; e += 32) s += red[e / cpg][g * cpg + e % cpg];
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if ((threadIdx.x & 31) == 0) {
-      sum[g] = s;
-      if (blocks == 1) total[g] = s;
-    }
+    if (g < p.groups)
+      for (int e = mine; e < count; e += team) s += value(g, e);
+    for (int o = team >> 1; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (g < p.groups && mine == 0) last(g, s);
   }
-  if (blocks > 1) {
+}
+// result(sum) of each group over the columns (and warps) of red and over the cluster, into total.
+template <class R>
+__device__ __forceinline__ void sum_groups(const Place& p, const Slabs& f, const float (*red)[kSlabColumns], float* sum,
+                                           float* total, R&& result) {
+  __syncthreads();
+  const auto value = [&](int g, int e) {
+    const int w = group_of(f, e);
+    return red[w][g * p.cpg + e - w * p.cpg];
+  };
+  const int count = (int)(blockDim.x >> 5) * p.cpg;
+  if (f.blocks == 1) {
+    team_sums(p, f.team, count, value, [&](int g, float s) { total[g] = result(g, s); });
+  } else {
+    team_sums(p, f.team, count, value, [&](int g, float s) { sum[g] = s; });
     __syncwarp();
     tc::cluster_sync();
     for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
       float s = 0.f;
-      for (int k = 0; k < blocks; ++k) s += tc::peer_load(tc::peer_addr(tc::smem_addr(sum + g), k));
-      total[g] = s;
+      for (int k = 0; k < f.blocks; ++k) s += tc::peer_load(tc::peer_addr(tc::smem_addr(sum + g), k));
+      total[g] = result(g, s);
     }
   }
   __syncthreads();
@@ -260,14 +281,14 @@ __device__ __forceinline__ void sum_groups(const Place& p, int cpg, int blocks, 
 
 template <int VEC, bool SILU, int ROWS>
 __global__ void __launch_bounds__(kFusedMost) norm_fused_kernel(NormArgs a, Slabs f) {
-  __shared__ FusedShared sh;
+  __shared__ __align__(16) FusedShared sh;
   const Place p = place_of<VEC>(a, f);
-  const int cpg = a.channels / a.groups, g0 = p.c0 / cpg;
+  const long long stat0 = (long long)p.sample * a.groups + p.g0;
   if (p.rows == 0) {
     if (p.part == 0)
       for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
-        a.mean[(long long)p.sample * a.groups + g0 + g] = 0.f;
-        a.rstd[(long long)p.sample * a.groups + g0 + g] = 1.f / sqrtf(a.eps);
+        a.mean[stat0 + g] = 0.f;
+        a.rstd[stat0 + g] = 1.f / sqrtf(a.eps);
       }
     return;  // every block of the cluster
   }
@@ -275,67 +296,95 @@ __global__ void __launch_bounds__(kFusedMost) norm_fused_kernel(NormArgs a, Slab
   const bool held = p.r1 - p.r0 <= step;
   Columns<VEC> c{};
   if (p.on) c.load_params(a, p.col);
+  const float* x = a.x + (long long)(p.r0 + p.ty) * a.x_stride + p.col;
+  const long long x_row = p.nty * a.x_stride, x_step = ROWS * x_row;
   Vec<VEC> v[ROWS];
-  auto read = [&](int base) {
+  const auto read = [&](const float* from, int left) {  // rows that are not there are zero
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const int r = base + p.ty + i * p.nty;
       v[i] = Vec<VEC>{};
-      if (p.on && r < p.r1) v[i] = load_vec<VEC>(a.x + r * a.x_stride + p.col);
+      if (p.on && i * p.nty < left) v[i] = load_vec<VEC>(from + i * x_row);
     }
   };
-  // this thread's rows: count, mean, squared deviations from it
+  const int rows_left = p.r1 - p.r0 - p.ty;  // of this thread, from its first row on
+  // the sums of this thread's rows; when they do not stay in registers also their
+  // count, mean and squared deviations from it
   float count = 0.f;
-  Vec<VEC> mean{}, dev{};
-  for (int base = p.r0; base < p.r1; base += step) {
-    read(base);
-    float n = 0.f;
-    Vec<VEC> s{}, d{};
+  Vec<VEC> mean{}, dev{}, sum{};
+  if (held) {
+    read(x, rows_left);
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      n += base + p.ty + i * p.nty < p.r1 ? 1.f : 0.f;
-      s = s + v[i];  // rows that are not there are zero
-    }
-    const Vec<VEC> m = s * all<VEC>(1.f / fmaxf(n, 1.f)), minus = m * all<VEC>(-1.f);
-#pragma unroll
-    for (int i = 0; i < ROWS; ++i)
-      if (base + p.ty + i * p.nty < p.r1) {
-        const Vec<VEC> q = v[i] + minus;
-        d = fma(q, q, d);
-      }
-    if (n > 0.f) {  // join with the rows before
-      const float sum = count + n;
-      const Vec<VEC> q = m + mean * all<VEC>(-1.f);
-      mean = fma(q, all<VEC>(n / sum), mean);
-      dev = fma(q * q, all<VEC>(count * n / sum), dev + d);
-      count = sum;
-    }
-  }
-  const float all_values = float(p.rows) * float(cpg);
-  sum_rows<VEC>(mean * all<VEC>(p.on ? count : 0.f), p, f.lanes, sh.red[0]);
-  sum_groups(p, cpg, f.blocks, sh.red[0], sh.sum[0], sh.total[0]);
-#pragma unroll
-  for (int j = 0; j < VEC; ++j) c.minus_mean.v[j] = p.on ? -(sh.total[0][(p.lane * VEC + j) / cpg] / all_values) : 0.f;
-  const Vec<VEC> q = mean + c.minus_mean;
-  sum_rows<VEC>(fma(q * q, all<VEC>(p.on ? count : 0.f), dev), p, f.lanes, sh.red[1]);
-  sum_groups(p, cpg, f.blocks, sh.red[1], sh.sum[1], sh.total[1]);
-  if (p.part == 0)
-    for (int g = threadIdx.x; g < p.groups; g += blockDim.x) {
-      const long long k = (long long)p.sample * a.groups + g0 + g;
-      a.mean[k] = sh.total[0][g] / all_values;
-      a.rstd[k] = 1.f / sqrtf(sh.total[1][g] / all_values + a.eps);
-    }
-  if (p.on) {
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) c.rstd.v[j] = 1.f / sqrtf(sh.total[1][(p.lane * VEC + j) / cpg] / all_values + a.eps);
-    for (int base = p.r0; base < p.r1; base += step) {
-      if (!held) read(base);
+    for (int i = 0; i < ROWS; ++i) sum = sum + v[i];
+  } else {
+    const float* from = x;
+    for (int left = rows_left; left > 0; left -= step, from += x_step) {
+      read(from, left);
+      float n = 0.f;
+      Vec<VEC> s{}, d{};
 #pragma unroll
       for (int i = 0; i < ROWS; ++i) {
-        const int r = base + p.ty + i * p.nty;
-        if (r < p.r1)
-          store_vec<VEC>(a.y + r * a.y_stride + p.col, activate<SILU>(fma(c.gamma, c.normalised(v[i]), c.beta)));
+        n += i * p.nty < left ? 1.f : 0.f;
+        s = s + v[i];
       }
+      const Vec<VEC> m = s * all<VEC>(1.f / n), minus = m * all<VEC>(-1.f);
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+        if (i * p.nty < left) {
+          const Vec<VEC> q = v[i] + minus;
+          d = fma(q, q, d);
+        }
+      const float both = count + n;  // join with the rows before
+      const Vec<VEC> q = m + mean * all<VEC>(-1.f);
+      mean = fma(q, all<VEC>(n / both), mean);
+      dev = fma(q * q, all<VEC>(count * n / both), dev + d);
+      count = both;
+    }
+    sum = mean * all<VEC>(count);
+  }
+  const float per_value = float(p.rows) * float(p.cpg);
+  sum_rows<VEC>(sum, p, f.lanes, sh.red[0]);
+  sum_groups(p, f, sh.red[0], sh.sum[0], sh.total[0], [&](int g, float s) {
+    const float m = s / per_value;
+    if (p.part == 0) a.mean[stat0 + g] = m;
+    return -m;
+  });
+  int group[VEC];  // of this thread's columns
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) group[j] = p.on ? group_of(f, p.lane * VEC + j) : 0;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) c.minus_mean.v[j] = sh.total[0][group[j]];
+  if (held) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i)
+      if (i * p.nty < rows_left && p.on) {
+        v[i] = v[i] + c.minus_mean;
+        dev = fma(v[i], v[i], dev);
+      }
+  } else if (p.on) {
+    const Vec<VEC> q = mean + c.minus_mean;
+    dev = fma(q * q, all<VEC>(count), dev);
+  }
+  sum_rows<VEC>(dev, p, f.lanes, sh.red[1]);
+  sum_groups(p, f, sh.red[1], sh.sum[1], sh.total[1], [&](int g, float s) {
+    const float r = 1.f / sqrtf(s / per_value + a.eps);
+    if (p.part == 0) a.rstd[stat0 + g] = r;
+    return r;
+  });
+  if (p.on) {
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) c.rstd.v[j] = sh.total[1][group[j]];
+    const Vec<VEC> w = c.gamma * c.rstd;
+    float* y = a.y + (long long)(p.r0 + p.ty) * a.y_stride + p.col;
+    const long long y_row = p.nty * a.y_stride, y_step = ROWS * y_row;
+    for (int left = rows_left; left > 0; left -= step, x += x_step, y += y_step) {
+      if (!held) {
+        read(x, left);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) v[i] = v[i] + c.minus_mean;
+      }
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+        if (i * p.nty < left) store_vec<VEC>(y + i * y_row, activate<SILU>(fma(w, v[i], c.beta)));
     }
   }
   if (f.blocks > 1) {
@@ -348,10 +397,9 @@ __global__ void __launch_bounds__(kFusedMost) norm_fused_kernel(NormArgs a, Slab
 template <int VEC, bool SILU, int ROWS>
 __global__ void __launch_bounds__(kFusedMost) norm_bwd_fused_kernel(NormArgs a, Slabs f, float2* __restrict__ slots) {
   grid_dependents_launch();
-  __shared__ FusedShared sh;
+  __shared__ __align__(16) FusedShared sh;
   const Place p = place_of<VEC>(a, f);
-  const int cpg = a.channels / a.groups;
-  float2* slot = slots + ((long long)p.sample * f.blocks + p.part) * a.channels + p.c0;
+  float2* slot = slots + (((long long)p.sample << f.shift) + p.part) * a.channels + p.c0;
   if (p.rows == 0) {
     for (int k = threadIdx.x; k < p.columns; k += blockDim.x) slot[k] = make_float2(0.f, 0.f);
     return;  // every block of the cluster
@@ -359,71 +407,75 @@ __global__ void __launch_bounds__(kFusedMost) norm_bwd_fused_kernel(NormArgs a, 
   const int step = p.nty * ROWS;
   const bool held = p.r1 - p.r0 <= step;
   Columns<VEC> c{};
+  int group[VEC];  // of this thread's columns
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) group[j] = p.on ? group_of(f, p.lane * VEC + j) : 0;
   if (p.on) {
     c.load_params(a, p.col);
-    c.load_stats(a, p.col, p.sample);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const long long k = (long long)p.sample * a.groups + p.g0 + group[j];
+      c.minus_mean.v[j] = -a.mean[k];
+      c.rstd.v[j] = a.rstd[k];
+    }
   }
+  const float* x = a.x + (long long)(p.r0 + p.ty) * a.x_stride + p.col;
+  const float* gy = a.grad_y + (long long)(p.r0 + p.ty) * a.gy_stride + p.col;
+  const long long x_row = p.nty * a.x_stride, gy_row = p.nty * a.gy_stride;
   Vec<VEC> h[ROWS], gz[ROWS];
-  auto read = [&](int base) {
+  const auto read = [&](const float* fx, const float* fg, int left) {  // rows that are not there are zero
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      const int r = base + p.ty + i * p.nty;
       h[i] = Vec<VEC>{};
       gz[i] = Vec<VEC>{};
-      if (p.on && r < p.r1) {
-        h[i] = load_vec<VEC>(a.x + r * a.x_stride + p.col);
-        gz[i] = load_vec<VEC>(a.grad_y + r * a.gy_stride + p.col);
+      if (p.on && i * p.nty < left) {
+        h[i] = load_vec<VEC>(fx + i * x_row);
+        gz[i] = load_vec<VEC>(fg + i * gy_row);
       }
     }
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
-      if (base + p.ty + i * p.nty < p.r1) {
+      if (i * p.nty < left) {
         h[i] = c.normalised(h[i]);
         gz[i] = activate_grad<SILU>(fma(c.gamma, h[i], c.beta), gz[i]);
       }
     }
   };
+  const int rows_left = p.r1 - p.r0 - p.ty;  // of this thread, from its first row on
   Vec<VEC> s1{}, s2{};
-  for (int base = p.r0; base < p.r1; base += step) {
-    read(base);
+  {
+    const float *fx = x, *fg = gy;
+    for (int left = rows_left; left > 0; left -= step, fx += ROWS * x_row, fg += ROWS * gy_row) {
+      read(fx, fg, left);
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      s1 = s1 + gz[i];
-      s2 = fma(gz[i], h[i], s2);
+      for (int i = 0; i < ROWS; ++i) {
+        s1 = s1 + gz[i];
+        s2 = fma(gz[i], h[i], s2);
+      }
     }
   }
   sum_rows<VEC>(s1, p, f.lanes, sh.red[0]);
   sum_rows<VEC>(s2, p, f.lanes, sh.red[1]);
   __syncthreads();
   for (int k = threadIdx.x; k < p.columns; k += blockDim.x) {
-    float x = 0.f, y = 0.f;
+    float u = 0.f, q = 0.f;
+#pragma unroll 4
     for (int w = 0; w < (int)(blockDim.x >> 5); ++w) {
-      x += sh.red[0][w][k];
-      y += sh.red[1][w][k];
+      u += sh.red[0][w][k];
+      q += sh.red[1][w][k];
     }
-    slot[k] = make_float2(x, y);
+    slot[k] = make_float2(u, q);
     const float w = a.gamma == nullptr ? 1.f : a.gamma[p.c0 + k];
-    sh.col[0][k] = w * x;
-    sh.col[1][k] = w * y;
+    sh.col[0][k] = w * u;
+    sh.col[1][k] = w * q;
   }
-  __syncthreads();
   if (a.grad_x == nullptr) return;  // every block
-  for (int g = threadIdx.x >> 5; g < p.groups; g += blockDim.x >> 5) {
-    float x = 0.f, y = 0.f;
-    for (int e = threadIdx.x & 31; e < cpg; e += 32) {
-      x += sh.col[0][g * cpg + e];
-      y += sh.col[1][g * cpg + e];
-    }
+  __syncthreads();
+  const float per_value = -1.f / (float(p.rows) * float(p.cpg));
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      x += __shfl_xor_sync(0xffffffffu, x, o);
-      y += __shfl_xor_sync(0xffffffffu, y, o);
-    }
-    if ((threadIdx.x & 31) == 0) {
-      sh.sum[0][g] = sh.total[0][g] = x;
-      sh.sum[1][g] = sh.total[1][g] = y;
-    }
-  }
+  for (int q = 0; q < 2; ++q)
+    team_sums(p, f.team, p.cpg, [&](int g, int e) { return sh.col[q][g * p.cpg + e]; },
+              [&](int g, float s) { (f.blocks > 1 ? sh.sum : sh.total)[q][g] = s * per_value; });
   if (f.blocks > 1) {
     __syncwarp();
     tc::cluster_sync();
@@ -436,21 +488,20 @@ __global__ void __launch_bounds__(kFusedMost) norm_bwd_fused_kernel(NormArgs a, 
   }
   __syncthreads();
   if (p.on) {
-    const float all_values = float(p.rows) * float(cpg);
-    Vec<VEC> m1, m2;
+    Vec<VEC> m1, m2;  // less the means of t and t h
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
-      m1.v[j] = -(sh.total[0][(p.lane * VEC + j) / cpg] / all_values);
-      m2.v[j] = -(sh.total[1][(p.lane * VEC + j) / cpg] / all_values);
+      m1.v[j] = sh.total[0][group[j]];
+      m2.v[j] = sh.total[1][group[j]];
     }
-    for (int base = p.r0; base < p.r1; base += step) {
-      if (!held) read(base);
+    float* gx = a.grad_x + (long long)(p.r0 + p.ty) * a.gx_stride + p.col;
+    const long long gx_row = p.nty * a.gx_stride;
+    for (int left = rows_left; left > 0; left -= step, x += ROWS * x_row, gy += ROWS * gy_row, gx += ROWS * gx_row) {
+      if (!held) read(x, gy, left);
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i) {
-        const int r = base + p.ty + i * p.nty;
-        if (r < p.r1)
-          store_vec<VEC>(a.grad_x + r * a.gx_stride + p.col, c.rstd * fma(h[i], m2, fma(c.gamma, gz[i], m1)));
-      }
+      for (int i = 0; i < ROWS; ++i)
+        if (i * p.nty < left)
+          store_vec<VEC>(gx + i * gx_row, c.rstd * fma(h[i], m2, fma(c.gamma, gz[i], m1)));
     }
   }
   if (f.blocks > 1) {
@@ -840,12 +891,16 @@ bool vec4_rows(const void* p, long long stride) { return stride % 4 == 0 && ((ui
 
 // The fused split for these sizes, or count = 0 for the tiles.  Measured on
 // fp32 rows with SiLU, forward / backward in microseconds:
-//   256 samples x 30 rows x 128 channels: whole rows, 256 threads, 4 rows each 7 / 8 (tiles 20 / 26);
-//   254 samples, 130 000 rows x 256: 128-byte slabs 88 / 119 (whole rows 119 / 150, tiles 96 / 157);
-//   4 000 samples, 130 000 rows x 256: whole rows, 128 threads 137 / 144, 256 threads 189 / 175 (tiles 255 / 347);
-//   61 samples, 131 101 rows x 256: 64-byte slabs 104 / 154, the tiles 86 / 145;
-//   1 sample of 130 000 rows x 256: a cluster of 8 per 64-byte slab 88 / 150, the tiles 78 / 126;
-//   1 sample of 20 000 rows x 128: a cluster of 8 per 64-byte slab 15 / 20, the tiles 14 / 23 in five launches.
+//   256 samples x 30 rows x 128 channels: whole rows, 256 threads, 4 rows each 4.6 / 6.9 (tiles 20 / 26);
+//   254 samples, 130 000 rows x 256: 128-byte slabs 59 / 105 (whole rows in clusters of 4 84 / 124, tiles 96 / 157);
+//   4 000 samples, 130 000 rows x 256: whole rows 83 / 132 (256-byte slabs 113 / 159, 128-byte ones 190 / 245);
+//   61 samples, 131 101 rows x 256: 64-byte slabs 98 / 164, the tiles 85 / 143;
+//   1 sample of 130 000 rows x 256: a cluster of 8 per 128-byte slab 110 / 174, the tiles 75 / 122;
+//   1 sample of 20 000 rows x 128: a cluster of 8 per 64-byte slab 13 / 20, the tiles 14 / 23 in five launches.
+// Index arithmetic and reductions that every thread repeats are what small
+// samples pay for: group numbers by a product, row addresses by steps and one
+// thread per statistic took the forward from 6.6 to 4.6 and, at 4 000 samples,
+// from 137 to 83.
 // So slabs narrow, down to 64 bytes a row, while the usual sample does not fit
 // the registers and there are not yet many blocks; then few blocks become a
 // cluster of larger ones.  Long samples of a tensor that leaves L2 go to the
@@ -877,6 +932,7 @@ Slabs fused_slabs(const NormArgs& a, int max_rows) {
   auto blocks = [&]() { return (long long)a.samples * f.count; };
   f.threads = 256;
   f.rows = 8;
+  f.per_cpg = ((1u << 20) + cpg - 1) / cpg;
   set(most / (unit * cpg) * unit);
   while (f.groups > unit && f.groups * cpg > 16 && blocks() < kManyBlocks && (held() < usual || blocks() < kFewBlocks)) {
     const int half = (f.groups / unit + 1) / 2 * unit;
@@ -891,6 +947,9 @@ Slabs fused_slabs(const NormArgs& a, int max_rows) {
     if (held() / 2 >= usual) f.rows = 4;  // small samples
     while (f.threads > 128 && held() / 2 >= usual) f.threads /= 2;
   }
+  while (1 << f.shift < f.blocks) ++f.shift;
+  f.team = 32;
+  while (f.team > 1 && f.team * f.groups > f.threads) f.team /= 2;
   if (held() * f.blocks * (blocks() < 4 * kFewBlocks ? 8 : 32) < longest || blocks() * f.blocks > 0x7fffffffLL) f.count = 0;
   return f;
 }

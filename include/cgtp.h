@@ -523,7 +523,7 @@ typedef enum { CGTP_ACT_NONE = 0, CGTP_ACT_SILU = 1 } cgtp_act;
  * grad_x may be grad_y.  Rows outside every sample (before graph_ptr[0], behind
  * graph_ptr[n_samples]) have no part in any result and are left as they were.  Statistics
  * and sums in fp32 over deviations from the mean; fixed order (no atomics).
- * channels >= 1, a multiple of groups (CGTP_ERR_INVALID_ARG otherwise); n <= 2^30.
+ * channels >= 1, a multiple of groups (CGTP_ERR_INVALID_ARG otherwise); n and n_samples <= 2^30.
  * max_rows: a bound on the rows of a sample where the caller knows one, 0
  * otherwise; it chooses how the work is split, never the result's validity.
  * workspace: device, 256-byte aligned, of the size
