@@ -525,6 +525,195 @@ cudaError_t launch_small(int batch, int rows, int cols, int steps, float scale, 
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// ------------------------------------------------------------- few entries
+// Matrices whose products are some ten thousand multiplications: a tensor-core
+// product of 128 rows and its way through tensor memory take about 1 us whatever
+// they hold, plain fp32 sums in shared memory less.  One block per matrix; KP
+// is the number of rows, rounded up to a power of two (the others are zero).
+// X, A and P = b A + c A A lie in shared memory by rows whose strides are odd
+// multiples of 16 bytes (no two of eight rows share banks); a thread sums a 2 x 2
+// tile of A or P, or a 2 x 4 tile of X, with `team` threads sharing the long sums.
+constexpr int kFewRows = 32;
+constexpr int kFewThreads = 512;
+
+struct FewLayout {
+  int quads, stride, bytes;  // groups of four columns; floats from row to row of X
+};
+__host__ __device__ inline FewLayout few_layout(int kp, int n) {
+  FewLayout L;
+  L.quads = (n + 3) / 4;
+  L.stride = 4 * (L.quads | 1);
+  L.bytes = (int)sizeof(float) * (2 * kp * L.stride + 2 * kp * (kp + 4));
+  return L;
+}
+
+// out(i, j, sum over the columns of x_i x_j) for all rows i, j.
+template <int KP, class F>
+__device__ __forceinline__ void few_gram(const float* x, int stride, int quads, int team_shift, F&& out) {
+  constexpr int H = KP / 2;
+  const int team = 1 << team_shift, mine = threadIdx.x & (team - 1);
+  for (int t0 = 0; t0 < H * H; t0 += blockDim.x >> team_shift) {  // the same for every thread
+    const int t = t0 + (threadIdx.x >> team_shift), i = t % H, j = t / H;
+    float s[2][2] = {};
+    if (t < H * H)
+      for (int q = mine; q < quads; q += team) {
+        float4 u[2], v[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          u[k] = *reinterpret_cast<const float4*>(x + (i + k * H) * stride + 4 * q);
+          v[k] = *reinterpret_cast<const float4*>(x + (j + k * H) * stride + 4 * q);
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+          for (int l = 0; l < 2; ++l)
+            s[k][l] = fmaf(u[k].w, v[l].w, fmaf(u[k].z, v[l].z, fmaf(u[k].y, v[l].y, fmaf(u[k].x, v[l].x, s[k][l]))));
+      }
+    for (int o = team >> 1; o > 0; o >>= 1)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k >> 1][k & 1] += __shfl_xor_sync(0xffffffffu, s[k >> 1][k & 1], o);
+    if (t < H * H && mine == 0)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) out(i + (k >> 1) * H, j + (k & 1) * H, s[k >> 1][k & 1]);
+  }
+}
+
+template <int KP>
+__global__ void __launch_bounds__(kFewThreads) ortho_few_kernel(SmallArgs a, int gram_shift, int square_shift) {
+  extern __shared__ __align__(16) float few_smem[];
+  __shared__ double sums[kFewThreads / 32];
+  constexpr int H = KP / 2, kStride = KP + 4;
+  const FewLayout L = few_layout(KP, a.n);
+  float *x = few_smem, *y = x + KP * L.stride, *gram = y + KP * L.stride, *p = gram + KP * kStride;
+  const int tid = threadIdx.x, lane = tid & 31, warps = blockDim.x >> 5;
+  const float* g = a.g + (long long)blockIdx.x * a.rows * a.cols;
+  float* out = a.out + (long long)blockIdx.x * a.rows * a.cols;
+  // X once from memory; squares in 64 bits, which neither overflow nor vanish
+  const int width = 4 * L.quads;
+  const auto place = [&](int q, int& r, int& c) {
+    if (a.tall) {
+      r = q % KP;
+      c = q / KP;
+    } else {
+      r = q / width;
+      c = q - r * width;
+    }
+  };
+  double s = 0.0;
+#pragma unroll 4
+  for (int q = tid; q < KP * width; q += blockDim.x) {
+    int r, c;
+    place(q, r, c);
+    const float v = r < a.m && c < a.n ? g[a.tall ? (long long)c * a.cols + r : (long long)r * a.cols + c] : 0.f;
+    x[r * L.stride + c] = v;
+    s = fma((double)v, (double)v, s);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) sums[tid >> 5] = s;
+  __syncthreads();
+  s = 0.0;
+  for (int w = 0; w < warps; ++w) s += sums[w];
+  // 1 / norm as f 2^(e1 + e2), each factor a normal fp32 number
+  int e;
+  const float f = (float)frexp(1.0 / (sqrt(s) + kNsEps), &e);
+  const float s1 = ldexpf(1.f, e / 2), s2 = ldexpf(f, e - e / 2);
+  for (int q = tid; q < KP * width; q += blockDim.x) {  // each thread its own
+    int r, c;
+    place(q, r, c);
+    x[r * L.stride + c] *= s1 * s2;
+  }
+  for (int step = 1; step <= a.steps; ++step) {
+    __syncthreads();
+    few_gram<KP>(x, L.stride, L.quads, gram_shift, [&](int i, int j, float v) { gram[i * kStride + j] = v; });
+    __syncthreads();
+    few_gram<KP>(gram, kStride, KP / 4, square_shift, [&](int i, int j, float v) {  // A is symmetric
+      p[i * kStride + j] = fmaf(kNsB, gram[i * kStride + j], kNsC * v);
+    });
+    __syncthreads();
+    for (int t = tid; t < H * L.quads; t += blockDim.x) {
+      const int i = t % H, q = t / H;
+      float4 w[2] = {};
+#pragma unroll
+      for (int l = 0; l < KP; l += 4) {
+        float4 b[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) b[k] = *reinterpret_cast<const float4*>(p + (i + k * H) * kStride + l);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          const float4 v = *reinterpret_cast<const float4*>(x + (l + d) * L.stride + 4 * q);
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float m = d == 0 ? b[k].x : d == 1 ? b[k].y : d == 2 ? b[k].z : b[k].w;
+            w[k] = make_float4(fmaf(m, v.x, w[k].x), fmaf(m, v.y, w[k].y), fmaf(m, v.z, w[k].z), fmaf(m, v.w, w[k].w));
+          }
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int r = i + k * H;
+        const float4 v = *reinterpret_cast<const float4*>(x + r * L.stride + 4 * q);
+        w[k] = make_float4(fmaf(kNsA, v.x, w[k].x), fmaf(kNsA, v.y, w[k].y), fmaf(kNsA, v.z, w[k].z), fmaf(kNsA, v.w, w[k].w));
+        if (step < a.steps) {
+          *reinterpret_cast<float4*>(y + r * L.stride + 4 * q) = w[k];
+        } else if (r < a.m) {
+          const float o[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+#pragma unroll
+          for (int d = 0; d < 4; ++d)
+            if (4 * q + d < a.n)
+              out[a.tall ? (long long)(4 * q + d) * a.cols + r : (long long)r * a.cols + 4 * q + d] = a.scale * o[d];
+        }
+      }
+    }
+    float* z = x;
+    x = y;
+    y = z;
+  }
+}
+
+// Rows of X that the kernel above is made for, or 0.  Five steps against the tensor cores', in us:
+// 5 x 8 x 8: 6.0 against 15.1; 64 x 16 x 16: 7.9, 14.8; 8 x 128: 8.9, 21; 16 x 128: 13, 21; 32 x 32: 13, 17;
+// 32 x 64: 17.8, 19.0; 16 x 256: 19, 30; 8 x 1024: 24, 27; beyond kFewWork 16 x 512: 31, 27; 32 x 128: 29, 23.
+// Threads: 64 for the smallest (8 x 8: 5.7, 256 threads 5.9), 512 for long rows (16 x 256: 19, 256 threads 23),
+// 256 between and for 32 rows, whose 2 x 2 tiles they cover (32 x 32: 13, 512 threads 16).
+constexpr int kFewWork = 65536;
+int few_rows(int m, int n) {
+  if (m > kFewRows) return 0;
+  int kp = 4;
+  while (kp < m) kp *= 2;
+  return (long long)kp * kp * n <= kFewWork ? kp : 0;
+}
+
+cudaError_t launch_few(int batch, int rows, int cols, int steps, float scale, const float* g, float* out,
+                       cudaStream_t stream) {
+  SmallArgs a{};
+  a.rows = rows;
+  a.cols = cols;
+  a.steps = steps;
+  a.tall = rows > cols;
+  a.m = a.tall ? cols : rows;
+  a.n = a.tall ? rows : cols;
+  a.scale = scale;
+  a.g = g;
+  a.out = out;
+  const int kp = few_rows(a.m, a.n);
+  const FewLayout L = few_layout(kp, a.n);
+  const int work = kp * kp * a.n, threads = work <= 512 ? 64 : kp == 32 || work <= 8192 ? 256 : kFewThreads;
+  const auto shift = [&](int quads) {  // of the threads that share a sum
+    int s = 0;
+    while (s < 5 && (2 << s) * (kp / 2) * (kp / 2) <= threads && (2 << s) <= quads) ++s;
+    return s;
+  };
+  void (*kernel)(SmallArgs, int, int) = kp == 4   ? ortho_few_kernel<4>
+                                        : kp == 8  ? ortho_few_kernel<8>
+                                        : kp == 16 ? ortho_few_kernel<16>
+                                                   : ortho_few_kernel<32>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.bytes);
+  if (e != cudaSuccess) return e;
+  kernel<<<batch, threads, L.bytes, stream>>>(a, shift(L.quads), shift(kp / 4));
+  return cudaGetLastError();
+}
+
 // ------------------------------------------------------------- larger matrices
 // One launch per product, over 128 x 128 tiles of the result.  X, A and P lie in
 // the workspace as the operands' own shared-memory tiles (128 rows x 64 columns
@@ -928,13 +1117,15 @@ cudaError_t launch_large(int batch, int rows, int cols, int steps, float scale, 
 
 size_t ortho_workspace(int batch, int rows, int cols) {
   const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
-  return small_blocks(m, n) > 0 ? 0 : pad256(large_layout(batch, m, n).bytes);
+  return few_rows(m, n) > 0 || small_blocks(m, n) > 0 ? 0 : pad256(large_layout(batch, m, n).bytes);
 }
 
 cudaError_t launch_ortho(int batch, int rows, int cols, int steps, float scale, const float* g, float* out, void* ws,
                          cudaStream_t stream) {
   if (batch == 0 || rows == 0 || cols == 0) return cudaSuccess;
-  if (small_blocks(rows < cols ? rows : cols, rows < cols ? cols : rows) > 0)
+  const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
+  if (few_rows(m, n) > 0) return launch_few(batch, rows, cols, steps, scale, g, out, stream);
+  if (small_blocks(m, n) > 0)
     return launch_small(batch, rows, cols, steps, scale, g, out, stream);
   return launch_large(batch, rows, cols, steps, scale, g, out, ws, stream);
 }
