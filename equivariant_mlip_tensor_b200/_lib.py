@@ -102,7 +102,7 @@ def lib():
 
 def call(name, *args):
     """Call an entry point and raise CGTPError on a non-zero status."""
-    st = getattr(lib(), name)(*args)
+    st = getattr(_LIB or lib(), name)(*args)
     if st != 0:
         raise CGTPError(name, st, lib().cgtp_last_cuda_error())
     return st

@@ -168,8 +168,9 @@ def _at(t):
 
 
 def _same_device(dev, *named):
+    index = dev.index
     for name, t in named:
-        if t is not None and t.device != dev:
+        if t is not None and t.get_device() != index:
             raise ValueError(f"{name} must be on {dev}, got {t.device}")
 
 
@@ -194,8 +195,10 @@ def _check_rows(t, name, n=None, width=None):
 
 
 def _check_vector(t, dtype, name, size):
+    if t is None:
+        return
     _check(t, dtype, name)
-    if t is not None and (t.dim() != 1 or t.numel() != size):
+    if t.shape != (size,):
         raise ValueError(f"{name} must have {size} elements, got {tuple(t.shape)}")
 
 
@@ -203,18 +206,20 @@ def _current_stream(index):
     return torch.cuda.current_stream(index).cuda_stream
 
 
-# the same number without a stream object around it, where this torch has the short way (2 us a call)
+# the same numbers without a stream object around them, where this torch has the short ways (2 us a call); a
+# tensor on the device is there before, so CUDA is initialised
 _current_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _call_on(dev, name, *args):
     """Call an entry point on the tensors' device and that device's current stream."""
-    stream = _current_stream(dev.index)
-    if dev.index == torch.cuda.current_device():
-        call(name, *args, stream)
+    index = dev.index
+    if index == _current_device():
+        call(name, *args, _current_stream(index))
     else:
         with torch.cuda.device(dev):
-            call(name, *args, stream)
+            call(name, *args, _current_stream(index))
 
 
 def _workspace(workspace, need, dev):

@@ -548,9 +548,11 @@ template <int ITEMS>
 static cudaError_t sort_block(int n, int n_rows, int passes, const int* tokens, int* order, int* sorted,
                               cudaStream_t stream) {
   constexpr int bytes = sizeof(int) * (2 * kBlockThreads * ITEMS + kBlockThreads / 32 * kDigits);
-  const cudaError_t e =
-      cudaFuncSetAttribute(sort_block_kernel<ITEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  if (e != cudaSuccess) return e;
+  if (bytes > 48 * 1024) {  // more than a block gets unasked
+    const cudaError_t e =
+        cudaFuncSetAttribute(sort_block_kernel<ITEMS>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+  }
   sort_block_kernel<ITEMS><<<1, kBlockThreads, bytes, stream>>>(n, n_rows, passes, tokens, order, sorted);
   return cudaGetLastError();
 }

@@ -708,8 +708,10 @@ cudaError_t launch_few(int batch, int rows, int cols, int steps, float scale, co
                                         : kp == 8  ? ortho_few_kernel<8>
                                         : kp == 16 ? ortho_few_kernel<16>
                                                    : ortho_few_kernel<32>;
-  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.bytes);
-  if (e != cudaSuccess) return e;
+  if (L.bytes > 48 * 1024) {  // more than a block gets unasked
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.bytes);
+    if (e != cudaSuccess) return e;
+  }
   kernel<<<batch, threads, L.bytes, stream>>>(a, shift(L.quads), shift(kp / 4));
   return cudaGetLastError();
 }
