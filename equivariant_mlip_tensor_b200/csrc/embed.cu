@@ -31,7 +31,7 @@ namespace {
 // stable.
 //
 // Up to kBlockTokens tokens: one block, all passes in shared memory, one launch
-// (7 680 tokens of 16 species: 8.0 us; the tiles take 6 us on the GPU in two launches, which
+// (7 680 tokens of 16 species: 8.0 us; the tiles take 5 us on the GPU in two launches, which
 // such a small batch does not hide).  Beyond: tiles of kSortTile tokens.  The
 // first launch counts each tile's digits; each pass is one more, in which every
 // tile adds up the counts of the tiles before it (and of smaller digits)
@@ -39,12 +39,16 @@ namespace {
 // (integer atomics: the counts do not depend on their order).  Beyond
 // kSortScanTiles tiles that sum over tiles, which every tile repeats, would
 // grow with their square: one more launch a pass then turns the counts into
-// prefixes first.
+// prefixes first (400 000 tokens, 196 tiles, two passes: 22.9 us without, 23.2
+// with; 600 000: 30.1, 27.3).  200 003 tokens of 50 021 rows take 20 us: count
+// 3, two passes of 8, mostly latency from one launch to the next and in its
+// chain of loads, ranks, prefix and scattered stores.
 constexpr int kSortThreads = 512;
 constexpr int kSortItems = 4;
 constexpr int kSortTile = kSortThreads * kSortItems;  // tokens per tile
 constexpr int kDigits = 256;
-constexpr int kSortScanTiles = 160;
+constexpr int kSortScanTiles = 200;
+constexpr int kSortGroups = kSortThreads / (kDigits / 4);  // of threads that add up the tiles' counts
 constexpr int kBlockThreads = 1024;
 constexpr int kBlockItems = 8;
 constexpr int kBlockTokens = kBlockThreads * kBlockItems;
@@ -220,50 +224,65 @@ __global__ void __launch_bounds__(kSortThreads)
                         int* __restrict__ pos_out, int* __restrict__ next_counts) {
   grid_dependents_launch();
   __shared__ int count[kSortThreads / 32][kDigits];
-  __shared__ int part[2][2][kDigits];  // [half of the tiles][before, all][digit]
+  __shared__ __align__(16) int part[kSortGroups][2][kDigits];  // [share of the tiles][before, all][digit]
   __shared__ int warp_sums[kDigits / 32];
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   for (int d = lane; d < kDigits; d += 32) count[w][d] = 0;
-  grid_dependency_wait();
   int key[kSortItems], pos[kSortItems], rank[kSortItems];
   const long long base = (long long)blockIdx.x * kSortTile + w * (32 * kSortItems);
+  if (keys_in == nullptr) {  // the tokens, which no launch of this call writes: before the wait
 #pragma unroll
-  for (int i = 0; i < kSortItems; ++i) {
-    const long long k = base + 32 * i + lane;
-    key[i] = -1;
-    pos[i] = 0;
-    if (k < n) {
-      key[i] = keys_in == nullptr ? token_key(tokens[k], n_rows) : keys_in[k];
-      pos[i] = pos_in == nullptr ? (int)k : pos_in[k];
+    for (int i = 0; i < kSortItems; ++i) {
+      pos[i] = (int)(base + 32 * i + lane);
+      key[i] = base + 32 * i + lane < n ? token_key(tokens[base + 32 * i + lane], n_rows) : -1;
+    }
+    grid_dependency_wait();
+  } else {
+    grid_dependency_wait();
+#pragma unroll
+    for (int i = 0; i < kSortItems; ++i) {
+      const long long k = base + 32 * i + lane;
+      key[i] = k < n ? keys_in[k] : -1;
+      pos[i] = k < n ? pos_in[k] : 0;
     }
   }
   // start of each digit of this tile: smaller digits of every tile, then the
-  // same digit of earlier tiles; each half of the threads adds up half of the tiles
-  const int d = tid & (kDigits - 1), half = tid / kDigits, tiles = gridDim.x;
-  int before = 0, all = 0;
-  if (tiles > kSortScanTiles) {  // prefixes already
-    if (half == 0) {
-      before = counts[(long long)blockIdx.x * kDigits + d];
-      all = counts[(long long)tiles * kDigits + d];
+  // same digit of earlier tiles; 64 threads of four digits each take every
+  // kSortGroups-th tile
+  const int d = tid & (kDigits - 1), tiles = gridDim.x;
+  const bool scanned = tiles > kSortScanTiles;  // the counts are prefixes already
+  if (!scanned) {
+    const int group = tid / (kDigits / 4), quad = tid % (kDigits / 4);
+    const int4* c = reinterpret_cast<const int4*>(counts) + quad;
+    int4 before = make_int4(0, 0, 0, 0), all = before;
+#pragma unroll 8
+    for (int b = group; b < tiles; b += kSortGroups) {
+      const int4 v = c[b * (kDigits / 4)];
+      all = make_int4(all.x + v.x, all.y + v.y, all.z + v.z, all.w + v.w);
+      if (b < (int)blockIdx.x) before = make_int4(before.x + v.x, before.y + v.y, before.z + v.z, before.w + v.w);
     }
-  } else {
-    const int b0 = half * tiles / 2, b1 = (half + 1) * tiles / 2;
-#pragma unroll 16
-    for (int b = b0; b < b1; ++b) {
-      const int c = counts[b * kDigits + d];
-      if (b < (int)blockIdx.x) before += c;
-      all += c;
-    }
+    reinterpret_cast<int4*>(part[group][0])[quad] = before;
+    reinterpret_cast<int4*>(part[group][1])[quad] = all;
   }
-  part[half][0][d] = before;
-  part[half][1][d] = all;
   __syncwarp();
   rank_digits(key, shift, digit_bits(n_rows, shift), count[w], rank);
   __syncthreads();
-  all = half == 0 ? part[0][1][d] + part[1][1][d] : 0;
+  int before = 0, all = 0;
+  if (tid < kDigits) {
+    if (scanned) {
+      before = counts[(long long)blockIdx.x * kDigits + d];
+      all = counts[(long long)tiles * kDigits + d];
+    } else {
+#pragma unroll
+      for (int g = 0; g < kSortGroups; ++g) {
+        before += part[g][0][d];
+        all += part[g][1][d];
+      }
+    }
+  }
   int run = prefix_digits(all, warp_sums);
-  if (half == 0) {  // the warps' counts become their starts
-    run += part[0][0][d] + part[1][0][d];
+  if (tid < kDigits) {  // the warps' counts become their starts
+    run += before;
 #pragma unroll
     for (int q = 0; q < kSortThreads / 32; ++q) {
       const int c = count[q][d];
@@ -354,9 +373,16 @@ __global__ void __launch_bounds__(kEmbedThreads, 4) embed_bwd_kernel(EmbedBwdArg
         }
         empty = lo >= a.n || a.sorted[lo] != r;
       }
-      for (unsigned m = __ballot_sync(0xffffffffu, empty); m != 0; m &= m - 1) {
+      const unsigned empties = __ballot_sync(0xffffffffu, empty);
+      const Vec<VEC> z{};
+      if (empties == 0xffffffffu) {  // 32 rows in one piece: few tokens for the table
+        float* rows = a.grad_table + r0 * (long long)a.width;
+#pragma unroll 4
+        for (long long c = wl * VEC; c < 32LL * a.width; c += 32 * VEC) store_vec<VEC>(rows + c, z);
+        continue;
+      }
+      for (unsigned m = empties; m != 0; m &= m - 1) {
         float* row = a.grad_table + (r0 + __ffs(m) - 1) * (long long)a.width;
-        Vec<VEC> z{};
         for (int c = wl * VEC; c < a.width; c += 32 * VEC) store_vec<VEC>(row + c, z);
       }
     }
@@ -526,13 +552,16 @@ int lanes_per_row(int width, int vec) {
   return l;
 }
 // Sorted positions per chunk, a function of the sizes alone (the sums' order
-// does not depend on the device): enough chunks for some 8 000 workers, at
-// least 16 positions so that the partial sums stay a small part of the reads.
+// does not depend on the device or on alignments).  Of the four blocks that an
+// SM holds, three are for chunks and one for the clearing, so that no block
+// starts late and runs alone at the end (200 003 x 256 of 50 021 rows: 417 + 148
+// blocks 53 us, 417 + 196 58 us; x 128: 391 + 196 33 us, 521 + 196 36 us).  At least 16
+// positions, so that the partial sums stay a small part of the reads.
 int embed_chunk(int n, int width) {
-  const long long slices = (width + 127) / 128;
-  int c = 16;
-  while (c < 256 && n * slices / c > 8192) c <<= 1;
-  return c;
+  const int vec = width % 4 == 0 ? 4 : 1, lpr = lanes_per_row(width, vec);
+  const long long slices = (width + lpr * vec - 1) / (lpr * vec), workers = 148LL * 3 * kEmbedThreads / lpr;
+  const long long c = ((n * slices + workers - 1) / workers + 7) / 8 * 8;
+  return c < 16 ? 16 : c > 256 ? 256 : (int)c;
 }
 
 }  // namespace
@@ -619,8 +648,9 @@ static cudaError_t embed_bwd(EmbedBwdArgs a, cudaStream_t stream) {
   a.lpr = lanes_per_row(a.width, VEC);
   a.slices = (a.width + a.lpr * VEC - 1) / (a.lpr * VEC);
   const long long blocks = ((long long)a.n_chunks * a.slices * a.lpr + kEmbedThreads - 1) / kEmbedThreads;
+  // a block searches kEmbedThreads rows at a time; one an SM while that takes each at most twice
   long long clear = ((long long)a.n_rows + kEmbedThreads - 1) / kEmbedThreads;
-  if (clear > 1024) clear = 1024;
+  if (clear > 148) clear = clear <= 2 * 148 ? 148 : clear > 1024 ? 1024 : clear;
   if (blocks + clear > 0x7fffffffLL || a.slices > 65535) return cudaErrorInvalidValue;
   embed_bwd_kernel<VEC><<<(unsigned)(blocks + clear), kEmbedThreads, 0, stream>>>(a, (int)clear);
   const cudaError_t e = cudaGetLastError();

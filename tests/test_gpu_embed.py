@@ -104,6 +104,20 @@ def test_scalar_block_of_features_in_place(api, width):
     assert not bool(wide[:, 0].any())
 
 
+@pytest.mark.parametrize("rows,width", [(40000, 12), (40003, 7), (300007, 8), (64, 260)])
+@pytest.mark.parametrize("n", [1, 40, 9000])
+def test_rows_without_a_token_are_cleared(api, rows, width, n):
+    """More rows than the clearing blocks search at once, in whole pieces of 32 rows and between tokens."""
+    import torch
+    rng = np.random.default_rng(rows + n)
+    tok = rng.integers(0, rows, n).astype(np.int32)
+    g = rng.standard_normal((n, width)).astype(np.float32)
+    out = torch.full((rows, width), float("nan"), device="cuda")
+    api.embed_backward(api.token_sort(cuda(tok), rows), cuda(g), out=out)
+    assert not out[torch.from_numpy(np.setdiff1d(np.arange(rows), tok)).cuda()].any()
+    _check_backward(out, tok, rows, g, 1.0)
+
+
 def test_long_sums_cross_many_chunks(api):
     """One row takes nearly every token: its sum is joined from hundreds of chunks."""
     rng = np.random.default_rng(3)
