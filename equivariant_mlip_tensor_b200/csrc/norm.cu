@@ -512,16 +512,19 @@ __global__ void __launch_bounds__(kFusedMost) norm_bwd_fused_kernel(NormArgs a, 
 
 // ------------------------------------------------------------------- tiles
 // The sample that row r belongs to: the last one that starts at or before r
-// (-1: none), found in log2(samples) steps.
+// (-1: none).  Whole warps call: 32 offsets at a time, so that 1 000 samples
+// take two loads in a row instead of ten.
 __device__ __forceinline__ int sample_of(const NormArgs& a, int r) {
   if (a.ptr == nullptr) return 0;
-  int lo = 0, hi = a.samples;  // first sample with ptr > r
+  const int lane = threadIdx.x & 31;
+  int lo = 0, hi = a.samples;  // the first sample with ptr > r is in [lo, hi]
   while (lo < hi) {
-    const int mid = lo + (hi - lo) / 2;
-    if (a.ptr[mid] <= r) lo = mid + 1;
-    else hi = mid;
+    const int step = (hi - lo + 31) / 32, at = lo + lane * step + step - 1;
+    const unsigned below = __ballot_sync(0xffffffffu, at < hi && a.ptr[at] <= r);
+    lo += __popc(below) * step;
+    hi = step == 1 ? lo : min(hi, lo + step - 1);
   }
-  return lo - 1;
+  return min(lo, a.samples) - 1;
 }
 
 // Calls f(sample, first row, last row + 1) for each part of the tile's rows
@@ -543,6 +546,23 @@ __device__ __forceinline__ void for_parts(const NormArgs& a, int r0, int r1, F&&
     }
     f(s, r, hi);
     r = hi;
+  }
+}
+
+// The same from the last row down.
+template <class F>
+__device__ __forceinline__ void for_parts_down(const NormArgs& a, int r0, int r1, F&& f) {
+  for (int r = r1 - 1; r >= r0;) {
+    const int s = sample_of(a, r);
+    if (s < 0) return;
+    const int2 b = sample_rows(a, s);
+    if (b.y <= r) {  // behind the last sample (or between samples of disordered offsets)
+      r = b.y - 1;
+      continue;
+    }
+    const int lo = min(max(b.x, r0), r);  // each step goes down, disordered offsets too
+    f(s, lo, r + 1);
+    r = lo - 1;
   }
 }
 
@@ -595,20 +615,24 @@ __global__ void __launch_bounds__(kNormThreads) norm_part_kernel(NormArgs a, int
     // this thread's rows: count, mean, squared deviations from it
     float count = 0.f;
     Vec<VEC> mean{}, dev{};
-    for (int base = lo + t.ty; base < hi; base += t.nty * kNormRows) {
-      Vec<VEC> v[kNormRows], sum{}, d{};
-      float n = 0.f;
+    const int step = t.nty * kNormRows;
+    const auto read = [&](Vec<VEC>(&v)[kNormRows], int base) {
 #pragma unroll
       for (int i = 0; i < kNormRows; ++i) {
         const int r = base + i * t.nty;
         v[i] = Vec<VEC>{};
         if (t.on && r < hi) v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
       }
+    };
+    const auto add = [&](const Vec<VEC>(&v)[kNormRows], int base) {
+      float n = 0.f;
+      Vec<VEC> sum{}, d{};
 #pragma unroll
       for (int i = 0; i < kNormRows; ++i) {
         n += base + i * t.nty < hi ? 1.f : 0.f;
         sum = sum + v[i];
       }
+      if (n == 0.f) return;
       const Vec<VEC> m = sum * all<VEC>(1.f / n), minus = m * all<VEC>(-1.f);
 #pragma unroll
       for (int i = 0; i < kNormRows; ++i)
@@ -622,6 +646,14 @@ __global__ void __launch_bounds__(kNormThreads) norm_part_kernel(NormArgs a, int
       mean = fma(q, all<VEC>(part), mean);
       dev = fma(q * q, all<VEC>(count * part), dev + d);
       count = both;
+    };
+    Vec<VEC> u[kNormRows], v[kNormRows];  // one is read while the other is used
+    read(u, lo + t.ty);
+    for (int base = lo + t.ty; base < hi; base += 2 * step) {
+      read(v, base + step);
+      add(u, base);
+      read(u, base + 2 * step);
+      add(v, base + step);
     }
     Vec<VEC> sum = mean * all<VEC>(count);
     __syncthreads();
@@ -717,17 +749,17 @@ __global__ void __launch_bounds__(TPI > 32 ? TPI : kNormThreads)
 template <int VEC, bool SILU>
 __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(NormArgs a, int lpr) {
   const Tile t = make_tile<VEC>(a, lpr, 1, gridDim.x - 1 - blockIdx.x);
-  if (!t.on) return;
   Vec<VEC> v[kNormRows];
 #pragma unroll
   for (int i = 0; i < kNormRows; ++i) {
     const int r = t.r0 + t.ty + i * t.nty;
-    if (r < t.r1) v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
+    if (t.on && r < t.r1) v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
   }
   Columns<VEC> c;
-  c.load_params(a, t.col);
+  if (t.on) c.load_params(a, t.col);
   grid_dependency_wait();
   for_parts(a, t.r0, t.r1, [&](int s, int lo, int hi) {
+    if (!t.on) return;
     c.load_stats(a, t.col, s);
 #pragma unroll
     for (int i = 0; i < kNormRows; ++i) {
@@ -738,36 +770,91 @@ __global__ void __launch_bounds__(kNormThreads) norm_apply_kernel(NormArgs a, in
   });
 }
 
+// A thread's rows of x and grad_y, every `step` rows from the first, on their way through
+// a ring of its own in shared memory: kRing rows are in flight while one is used, 192
+// KB an SM, without registers.  (A load takes some 2 to 3 us when the memory is busy, so 6.5
+// TB/s want 100 KB in flight an SM all the time.  The backward of 131 101 x 256 in 61 samples takes
+// 121 us so, 135 us with 8 rows in registers that are read in one go and then used, 150 us with two
+// halves of them in turn.)
+constexpr int kRing = 8;
+constexpr int kRingBlocks = 3;  // blocks an SM
+template <int VEC>
+constexpr int ring_bytes() {
+  return kRing * 2 * kNormThreads * VEC * (int)sizeof(float);
+}
+template <int VEC>
+struct RowRing {
+  const float *x, *g;
+  long long x_step, g_step;
+  int left;   // rows not yet under way
+  int place;  // of the next row
+  float* mine;
+  __device__ __forceinline__ RowRing(const NormArgs& a, float* ring, int row, int step, int rows, int col)
+      : x(a.x + row * a.x_stride + col),
+        g(a.grad_y + row * a.gy_stride + col),
+        x_step(step * a.x_stride),
+        g_step(step * a.gy_stride),
+        left(rows),
+        place(0),
+        mine(ring + threadIdx.x * VEC) {
+    for (int i = 0; i < kRing; ++i) next();
+  }
+  // The next row into the place of the one that was used.
+  __device__ __forceinline__ void next() {
+    if (left > 0) {
+      float* to = mine + place * (2 * kNormThreads * VEC);
+      copy(to, x);
+      copy(to + kNormThreads * VEC, g);
+      x += x_step;
+      g += g_step;
+      --left;
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    place = (place + 1) % kRing;
+  }
+  __device__ __forceinline__ void read(Vec<VEC>& vx, Vec<VEC>& vg) const {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    vx = load_vec<VEC>(mine + place * (2 * kNormThreads * VEC));
+    vg = load_vec<VEC>(mine + place * (2 * kNormThreads * VEC) + kNormThreads * VEC);
+  }
+  static __device__ __forceinline__ void copy(float* to, const float* from) {
+    if constexpr (VEC == 4)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(tc::smem_addr(to)), "l"(from) : "memory");
+    else
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_addr(to)), "l"(from) : "memory");
+  }
+  static __device__ __forceinline__ void finish() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+};
+// Rows of a tile that belong to the thread's row group.
+__device__ __forceinline__ int rows_of_group(const Tile& t) {
+  return t.on && t.r1 - t.r0 > t.ty ? (t.r1 - t.r0 - t.ty + t.nty - 1) / t.nty : 0;
+}
+
 // 1, backward: slot [channel] = (sum gz, sum gz h) of the part.
 template <int VEC, bool SILU>
-__global__ void __launch_bounds__(kNormThreads)
+__global__ void __launch_bounds__(kNormThreads, kRingBlocks)
     norm_bwd_part_kernel(NormArgs a, int lpr, int per, float2* __restrict__ slots) {
   grid_dependents_launch();
+  extern __shared__ __align__(16) float norm_ring[];
   __shared__ float red[2 * VEC * kNormThreads];
   const Tile t = make_tile<VEC>(a, lpr, per, blockIdx.x);
+  int row = t.r0 + t.ty;
+  RowRing<VEC> ring(a, norm_ring, row, t.nty, rows_of_group(t), t.col);
   Columns<VEC> c{};
   if (t.on) c.load_params(a, t.col);
   for_parts(a, t.r0, t.r1, [&](int s, int lo, int hi) {
     Vec<VEC> s1{}, s2{};
     if (t.on) {
       c.load_stats(a, t.col, s);
-      for (int base = lo + t.ty; base < hi; base += t.nty * kNormRows) {
-        Vec<VEC> v[kNormRows], g[kNormRows];
-#pragma unroll
-        for (int i = 0; i < kNormRows; ++i) {
-          const int r = base + i * t.nty;
-          if (r < hi) {
-            v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
-            g[i] = load_vec<VEC>(a.grad_y + r * a.gy_stride + t.col);
-          }
+      for (; row < hi; row += t.nty) {
+        Vec<VEC> x, g;
+        ring.read(x, g);
+        if (row >= lo) {
+          const Vec<VEC> h = c.normalised(x), gz = activate_grad<SILU>(fma(c.gamma, h, c.beta), g);
+          s1 = s1 + gz;
+          s2 = fma(gz, h, s2);
         }
-#pragma unroll
-        for (int i = 0; i < kNormRows; ++i)
-          if (base + i * t.nty < hi) {
-            const Vec<VEC> h = c.normalised(v[i]), gz = activate_grad<SILU>(fma(c.gamma, h, c.beta), g[i]);
-            s1 = s1 + gz;
-            s2 = fma(gz, h, s2);
-          }
+        ring.next();
       }
     }
     float sum[2 * VEC];
@@ -783,28 +870,27 @@ __global__ void __launch_bounds__(kNormThreads)
       for (int j = 0; j < VEC; ++j)
         slots[((long long)t.index + s) * a.channels + t.col + j] = make_float2(sum[j], sum[VEC + j]);
   });
+  ring.finish();
 }
 
-// 3, backward; the order of the tiles as in the forward
+// 3, backward: the tiles of step 1, their rows from the last to the first (what
+// step 1 read last is still in L2).  The rows, which no launch of this call
+// writes before, are under way before the wait for step 2.
 template <int VEC, bool SILU>
-__global__ void __launch_bounds__(kNormThreads)
-    norm_bwd_apply_kernel(NormArgs a, int lpr, const float2* __restrict__ terms) {
-  const Tile t = make_tile<VEC>(a, lpr, 1, gridDim.x - 1 - blockIdx.x);
-  if (!t.on) return;
-  Vec<VEC> v[kNormRows], g[kNormRows];
-#pragma unroll
-  for (int i = 0; i < kNormRows; ++i) {
-    const int r = t.r0 + t.ty + i * t.nty;
-    if (r < t.r1) {
-      v[i] = load_vec<VEC>(a.x + r * a.x_stride + t.col);
-      g[i] = load_vec<VEC>(a.grad_y + r * a.gy_stride + t.col);
-    }
-  }
-  Columns<VEC> c;
-  c.load_params(a, t.col);
+__global__ void __launch_bounds__(kNormThreads, kRingBlocks)
+    norm_bwd_apply_kernel(NormArgs a, int lpr, int per, const float2* __restrict__ terms) {
+  extern __shared__ __align__(16) float norm_ring[];
+  const Tile t = make_tile<VEC>(a, lpr, per, blockIdx.x);
+  int row = t.r1 - 1 - t.ty;
+  RowRing<VEC> ring(a, norm_ring, row, -t.nty, rows_of_group(t), t.col);
+  float* gx = a.grad_x + row * a.gx_stride + t.col;
+  const long long gx_step = t.nty * a.gx_stride;
+  Columns<VEC> c{};
+  if (t.on) c.load_params(a, t.col);
   grid_dependents_launch();
   grid_dependency_wait();
-  for_parts(a, t.r0, t.r1, [&](int s, int lo, int hi) {
+  for_parts_down(a, t.r0, t.r1, [&](int s, int lo, int hi) {
+    if (!t.on) return;
     c.load_stats(a, t.col, s);
     Vec<VEC> m1, m2;
 #pragma unroll
@@ -813,15 +899,17 @@ __global__ void __launch_bounds__(kNormThreads)
       m1.v[j] = -m.x;
       m2.v[j] = -m.y;
     }
-#pragma unroll
-    for (int i = 0; i < kNormRows; ++i) {
-      const int r = t.r0 + t.ty + i * t.nty;
-      if (r >= lo && r < hi) {
-        const Vec<VEC> h = c.normalised(v[i]), gz = activate_grad<SILU>(fma(c.gamma, h, c.beta), g[i]);
-        store_vec<VEC>(a.grad_x + r * a.gx_stride + t.col, c.rstd * fma(h, m2, fma(c.gamma, gz, m1)));
+    for (; row >= lo; row -= t.nty, gx -= gx_step) {
+      Vec<VEC> x, g;
+      ring.read(x, g);
+      if (row < hi) {
+        const Vec<VEC> h = c.normalised(x), gz = activate_grad<SILU>(fma(c.gamma, h, c.beta), g);
+        store_vec<VEC>(gx, c.rstd * fma(h, m2, fma(c.gamma, gz, m1)));
       }
+      ring.next();
     }
   });
+  ring.finish();
 }
 
 // -------------------------------------------------------------- parameters
@@ -894,8 +982,8 @@ bool vec4_rows(const void* p, long long stride) { return stride % 4 == 0 && ((ui
 //   256 samples x 30 rows x 128 channels: whole rows, 256 threads, 4 rows each 4.6 / 6.9 (tiles 20 / 26);
 //   254 samples, 130 000 rows x 256: 128-byte slabs 59 / 105 (whole rows in clusters of 4 84 / 124, tiles 96 / 157);
 //   4 000 samples, 130 000 rows x 256: whole rows 83 / 132 (256-byte slabs 113 / 159, 128-byte ones 190 / 245);
-//   61 samples, 131 101 rows x 256: 64-byte slabs 98 / 164, the tiles 85 / 143;
-//   1 sample of 130 000 rows x 256: a cluster of 8 per 128-byte slab 110 / 174, the tiles 75 / 122;
+//   61 samples, 131 101 rows x 256: 64-byte slabs 98 / 164, the tiles 80 / 121;
+//   1 sample of 130 000 rows x 256: a cluster of 8 per 128-byte slab 110 / 174, the tiles 71 / 116;
 //   1 sample of 20 000 rows x 128: a cluster of 8 per 64-byte slab 13 / 20, the tiles 14 / 23 in five launches.
 // Index arithmetic and reductions that every thread repeats are what small
 // samples pay for: group numbers by a product, row addresses by steps and one
@@ -970,10 +1058,11 @@ cudaError_t launch_cluster(void (*kernel)(P...), const NormArgs& a, const Slabs&
   return cudaLaunchKernelEx(&cfg, kernel, a, f, args...);
 }
 
-// Rows of a tile of step 1, as a multiple of a block's registers: some four
-// tiles an SM, so that few slots have to be joined.
-int part_rows(const NormArgs& a, int rows, unsigned columns) {
-  const long long blocks = tiles_of(a.n, rows) * columns, per = (blocks + 4 * kFewBlocks - 1) / (4 * kFewBlocks);
+// Rows of a tile of step 1, as a multiple of a block's registers: as many tiles as
+// are resident at once, `resident` blocks an SM (131 101 x 256: forward 80 us, with twice as many
+// tiles 84), which leaves few slots to join.
+int part_rows(const NormArgs& a, int rows, unsigned columns, int resident) {
+  const long long blocks = tiles_of(a.n, rows) * columns, per = (blocks + resident * kFewBlocks - 1) / (resident * kFewBlocks);
   return (int)(per < 1 ? 1 : per > 64 ? 64 : per);
 }
 
@@ -999,7 +1088,7 @@ cudaError_t norm_fwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t str
                        : launch_cluster(norm_fused_kernel<VEC, SILU, 8>, a, f, stream);
   const int lpr = lanes_per_row(a.channels, VEC), rows = rows_per_tile(a.channels, VEC);
   const unsigned columns = (unsigned)((a.channels + lpr * VEC - 1) / (lpr * VEC));
-  const int per = part_rows(a, rows, columns);
+  const int per = part_rows(a, rows, columns, 2);
   cudaError_t e = cudaSuccess;
   if (a.n > 0) {
     norm_part_kernel<VEC><<<dim3((unsigned)tiles_of(a.n, per * rows), columns), kNormThreads, 0, stream>>>(a, lpr, per,
@@ -1030,18 +1119,23 @@ cudaError_t norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t str
   }
   const int lpr = lanes_per_row(a.channels, VEC), rows = rows_per_tile(a.channels, VEC);
   const unsigned columns = (unsigned)((a.channels + lpr * VEC - 1) / (lpr * VEC));
-  const int per = part_rows(a, rows, columns);
+  const int per = part_rows(a, rows, columns, kRingBlocks);
+  constexpr int ring = ring_bytes<VEC>();
   const long long tiles = tiles_of(a.n, per * rows), n_slots = tiles + a.samples;
   cudaError_t e = cudaMemsetAsync(slots, 0, sizeof(float2) * (size_t)n_slots * a.channels, stream);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(norm_bwd_part_kernel<VEC, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(norm_bwd_apply_kernel<VEC, SILU>, cudaFuncAttributeMaxDynamicSharedMemorySize, ring);
   if (e == cudaSuccess && a.n > 0) {
-    norm_bwd_part_kernel<VEC, SILU><<<dim3((unsigned)tiles, columns), kNormThreads, 0, stream>>>(a, lpr, per, slots);
+    norm_bwd_part_kernel<VEC, SILU><<<dim3((unsigned)tiles, columns), kNormThreads, ring, stream>>>(a, lpr, per, slots);
     e = cudaGetLastError();
   }
   if (e == cudaSuccess && a.grad_x != nullptr && a.samples > 0) {
     e = join<true>(a, per * rows, slots, terms, stream);
     if (e == cudaSuccess && a.n > 0)
-      e = launch_kernel(norm_bwd_apply_kernel<VEC, SILU>, dim3((unsigned)tiles_of(a.n, rows), columns),
-                        dim3(kNormThreads), 0, stream, true, a, lpr, (const float2*)terms);
+      e = launch_kernel(norm_bwd_apply_kernel<VEC, SILU>, dim3((unsigned)tiles, columns), dim3(kNormThreads), ring,
+                        stream, true, a, lpr, per, (const float2*)terms);
   }
   return e != cudaSuccess ? e : sum_params(a, n_slots, slots, sums, a.n > 0, stream);
 }
