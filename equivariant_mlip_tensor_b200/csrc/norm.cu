@@ -980,11 +980,11 @@ bool vec4_rows(const void* p, long long stride) { return stride % 4 == 0 && ((ui
 // The fused split for these sizes, or count = 0 for the tiles.  Measured on
 // fp32 rows with SiLU, forward / backward in microseconds:
 //   256 samples x 30 rows x 128 channels: whole rows, 256 threads, 4 rows each 4.6 / 6.9 (tiles 20 / 26);
-//   254 samples, 130 000 rows x 256: 128-byte slabs 59 / 105 (whole rows in clusters of 4 84 / 124, tiles 96 / 157);
-//   4 000 samples, 130 000 rows x 256: whole rows 83 / 132 (256-byte slabs 113 / 159, 128-byte ones 190 / 245);
+//   254 samples, 130 000 rows x 256: 128-byte slabs 59 / 105 (whole rows in clusters of 4 84 / 124, tiles 80 / 124);
+//   4 000 samples, 130 000 rows x 256: whole rows 83 / 132 (256-byte slabs 113 / 159, tiles 270 / 241);
 //   61 samples, 131 101 rows x 256: 64-byte slabs 98 / 164, the tiles 80 / 121;
 //   1 sample of 130 000 rows x 256: a cluster of 8 per 128-byte slab 110 / 174, the tiles 71 / 116;
-//   1 sample of 20 000 rows x 128: a cluster of 8 per 64-byte slab 13 / 20, the tiles 14 / 23 in five launches.
+//   1 sample of 20 000 rows x 128: a cluster of 8 per 64-byte slab 13 / 20, the tiles 12 / 20 in three and six launches.
 // Index arithmetic and reductions that every thread repeats are what small
 // samples pay for: group numbers by a product, row addresses by steps and one
 // thread per statistic took the forward from 6.6 to 4.6 and, at 4 000 samples,
