@@ -9,7 +9,8 @@
 // which lifts small values by a and keeps every value in [0, 1.21]: it stays
 // bounded for any number of steps.
 //
-// The products run on the tensor cores in fp16 pairs: x 2^k = high + low holds 22
+// All but the smallest matrices (which sum in fp32) have their products on the
+// tensor cores in fp16 pairs: x 2^k = high + low holds 22
 // bits of x, and low high + high low + high high, summed in fp32, leaves out
 // only low low (2^-22 of a product and less), so three fp16 products give a
 // product of fp32 accuracy.  That the values stay bounded makes fixed powers
