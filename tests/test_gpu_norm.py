@@ -232,6 +232,33 @@ def test_infinite_value_leaves_no_number_in_its_group_of_a_long_sample(api):
     assert np.isnan(host(y)[n // 2:, 64:]).all() and np.isfinite(host(y)).sum() == n * c - n // 2 * 64
 
 
+@pytest.mark.parametrize("c", [132, 520, 35])
+@pytest.mark.parametrize("ptr", [[3, 40, 40, 700, 900], [0, 0, 1000, 1000], [998, 999], list(range(5, 991, 5))])
+def test_rows_outside_every_sample_of_wide_groups(api, c, ptr):
+    """Groups wider than a fused slab (tiles): rows before, behind and between what
+    belongs to a graph may hold anything, and are left as they were; in place and with a row stride."""
+    rng = np.random.default_rng(c)
+    n, wide = 1000, c + 4
+    x, gy = (rng.standard_normal((n, wide)).astype(np.float32) for _ in range(2))
+    m = _inside(ptr, n)
+    x[~m], gy[~m] = np.nan, np.inf
+    gamma, beta = rng.standard_normal(c).astype(np.float32), rng.standard_normal(c).astype(np.float32)
+    kw = dict(graph_ptr=_i32(ptr), activation="silu")
+    t, g = cuda(x), cuda(gy)
+    y, mean, rstd = api.group_norm_forward(t[:, :c], cuda(gamma), cuda(beta), 1, eps=EPS, **kw)
+    gx, gg, gb = api.group_norm_backward(t[:, :c], cuda(gamma), cuda(beta), 1, mean, rstd, g[:, :c], grad_x=g[:, :c], **kw)
+    clean = np.where(m[:, None], x, 0)[:, :c], np.where(m[:, None], gy, 0)[:, :c]
+    want, _, _, bound = _forward_bound(clean[0], gamma, beta, 1, ptr, "silu")
+    assert (np.abs(host(y) - want)[m] <= bound[m]).all()
+    wx, wg, wb = onorm.backward(clean[0], gamma, beta, 1, ptr, EPS, "silu", clean[1])
+    got = host(g)
+    assert np.array_equal(got[~m], gy[~m]) and np.array_equal(got[:, c:], gy[:, c:])
+    # graphs of one row and few channels: the gradient is what cancels, measured against its terms
+    scale = max(np.abs(wx[m]).max(), 0.1 * np.abs(gy[m][:, :c]).max() * np.abs(gamma).max())
+    assert np.abs(got[m][:, :c] - wx[m]).max() <= GRAD_TOL * scale
+    assert rel_err(host(gg), wg) <= GRAD_TOL and rel_err(host(gb), wb) <= GRAD_TOL
+
+
 def test_gradient_against_differences(api):
     """Directional differences of the kernel's own forward.
 
