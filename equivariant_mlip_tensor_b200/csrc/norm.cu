@@ -985,6 +985,8 @@ bool vec4_rows(const void* p, long long stride) { return stride % 4 == 0 && ((ui
 //   61 samples, 131 101 rows x 256: 64-byte slabs 98 / 164, the tiles 80 / 121;
 //   1 sample of 130 000 rows x 256: a cluster of 8 per 128-byte slab 110 / 174, the tiles 71 / 116;
 //   1 sample of 20 000 rows x 128: a cluster of 8 per 64-byte slab 13 / 20, the tiles 12 / 20 in three and six launches.
+//   400 samples of up to 3 013 rows, 200 000 rows x 64: 64-byte slabs 38 / 72, the tiles 47 / 58;
+//   100 samples of up to 2 441 rows, 60 000 rows x 256: 64-byte slabs 39 / 68, the tiles 44 / 57.
 // Index arithmetic and reductions that every thread repeats are what small
 // samples pay for: group numbers by a product, row addresses by steps and one
 // thread per statistic took the forward from 6.6 to 4.6 and, at 4 000 samples,
@@ -993,10 +995,11 @@ bool vec4_rows(const void* p, long long stride) { return stride % 4 == 0 && ((ui
 // the registers and there are not yet many blocks; then few blocks become a
 // cluster of larger ones.  Long samples of a tensor that leaves L2 go to the
 // tiles, which read whole rows, as do longest samples that would keep their
-// blocks reading long after the others.
+// blocks reading long after the others (in the backward, which reads twice as
+// much, sooner).
 constexpr long long kFewBlocks = 148, kManyBlocks = 8 * kFewBlocks;
 template <int VEC>
-Slabs fused_slabs(const NormArgs& a, int max_rows) {
+Slabs fused_slabs(const NormArgs& a, int max_rows, bool backward) {
   Slabs f{};
   const int cpg = a.channels / a.groups;
   const int most = VEC == 4 ? kSlabColumns : 32;  // 32 lanes across
@@ -1038,6 +1041,9 @@ Slabs fused_slabs(const NormArgs& a, int max_rows) {
   while (1 << f.shift < f.blocks) ++f.shift;
   f.team = 32;
   while (f.team > 1 && f.team * f.groups > f.threads) f.team /= 2;
+  if (backward && max_rows > 1024 && max_rows > 4 * average && max_rows > 4 * held() * f.blocks &&
+      (long long)a.n * a.channels > (8 << 20))
+    f.count = 0;
   if (held() * f.blocks * (blocks() < 4 * kFewBlocks ? 8 : 32) < longest || blocks() * f.blocks > 0x7fffffffLL) f.count = 0;
   return f;
 }
@@ -1062,7 +1068,7 @@ cudaError_t launch_cluster(void (*kernel)(P...), const NormArgs& a, const Slabs&
 // are resident at once, `resident` blocks an SM (131 101 x 256: forward 80 us, with twice as many
 // tiles 84), which leaves few slots to join.
 int part_rows(const NormArgs& a, int rows, unsigned columns, int resident) {
-  const long long blocks = tiles_of(a.n, rows) * columns, per = (blocks + resident * kFewBlocks - 1) / (resident * kFewBlocks);
+  const long long blocks = tiles_of(a.n, rows) * columns, most = resident * kFewBlocks, per = (blocks + most - 1) / most;
   return (int)(per < 1 ? 1 : per > 64 ? 64 : per);
 }
 
@@ -1082,7 +1088,7 @@ cudaError_t join(const NormArgs& a, int rows, const float2* slots, float2* terms
 
 template <int VEC, bool SILU>
 cudaError_t norm_fwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t stream) {
-  const Slabs f = fused_slabs<VEC>(a, max_rows);
+  const Slabs f = fused_slabs<VEC>(a, max_rows, false);
   if (f.count > 0)
     return f.rows == 4 ? launch_cluster(norm_fused_kernel<VEC, SILU, 4>, a, f, stream)
                        : launch_cluster(norm_fused_kernel<VEC, SILU, 8>, a, f, stream);
@@ -1111,7 +1117,7 @@ cudaError_t norm_bwd(const NormArgs& a, int max_rows, void* ws, cudaStream_t str
   float2* terms = (float2*)ws;
   float2* sums = (float2*)((char*)ws + terms_bytes(a));
   float2* slots = (float2*)((char*)ws + terms_bytes(a) + sums_bytes(a));
-  const Slabs f = fused_slabs<VEC>(a, max_rows);
+  const Slabs f = fused_slabs<VEC>(a, max_rows, true);
   if (f.count > 0) {
     const cudaError_t e = f.rows == 4 ? launch_cluster(norm_bwd_fused_kernel<VEC, SILU, 4>, a, f, stream, slots)
                                       : launch_cluster(norm_bwd_fused_kernel<VEC, SILU, 8>, a, f, stream, slots);
@@ -1149,8 +1155,8 @@ size_t norm_workspace(int n, int samples, int channels, int groups, int max_rows
   a.samples = samples;
   a.channels = channels;
   a.groups = groups;
-  const Slabs one = fused_slabs<1>(a, max_rows);
-  const Slabs four = channels % 4 == 0 ? fused_slabs<4>(a, max_rows) : one;
+  const Slabs one = fused_slabs<1>(a, max_rows, backward);
+  const Slabs four = channels % 4 == 0 ? fused_slabs<4>(a, max_rows, backward) : one;
   const bool fused = one.count > 0 && four.count > 0;
   if (fused && !backward) return 0;
   const int blocks = one.blocks > four.blocks ? one.blocks : four.blocks;
