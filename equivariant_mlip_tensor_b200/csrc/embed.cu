@@ -451,7 +451,7 @@ constexpr int kJoinShort = 256, kJoinLong = 1024;
 template <int VEC>
 __global__ void __launch_bounds__(kJoinLong) embed_join_kernel(EmbedBwdArgs a) {
   __shared__ Vec<VEC> part[kJoinLong];
-  __shared__ int long_run[kJoinShort];  // by chunk of the block: the row of a long run, or -1
+  __shared__ int2 long_run[kJoinShort];  // by chunk of the block: the row of a long run, or -1, and its last chunk
   const int lane = threadIdx.x & (a.lpr - 1), worker = threadIdx.x / a.lpr, workers = blockDim.x / a.lpr;
   const int col = (blockIdx.y * a.lpr + lane) * VEC, chunks = kJoinShort / a.lpr;
   const bool on = col < a.width;
@@ -474,6 +474,13 @@ __global__ void __launch_bounds__(kJoinLong) embed_join_kernel(EmbedBwdArgs a) {
       const int far = chunk + 1 + kShortRun;
       if (far < a.n_chunks && a.sorted[far * a.chunk] == key) {
         is_long = key;
+        int hi = a.n_chunks - 1;  // the last chunk that begins inside the run
+        last = far;
+        while (last < hi) {
+          const int mid = last + (hi - last + 1) / 2;
+          if (a.sorted[mid * a.chunk] == key) last = mid;
+          else hi = mid - 1;
+        }
       } else {
         run = key;
         for (int c = chunk + 1; c < far; ++c)  // chunks that begin inside the run
@@ -484,20 +491,15 @@ __global__ void __launch_bounds__(kJoinLong) embed_join_kernel(EmbedBwdArgs a) {
   grid_dependency_wait();
   if (run >= 0 && on) {
     Vec<VEC> s = load_vec<VEC>(a.tail + (long long)chunk * a.width + col);
+#pragma unroll 8
     for (int c = chunk + 1; c <= last; ++c) add(s, load_vec<VEC>(a.head + (long long)c * a.width + col));
     finish(run, s);
   }
-  if (lane == 0 && worker < chunks) long_run[worker] = is_long;
+  if (lane == 0 && worker < chunks) long_run[worker] = make_int2(is_long, last);
   if (!__syncthreads_or(is_long >= 0)) return;
   for (int w = 0; w < chunks; ++w) {
-    const int row = long_run[w], first = chunk0 + w;
+    const int row = long_run[w].x, lo = long_run[w].y, first = chunk0 + w;
     if (row < 0) continue;  // the same for every thread
-    int lo = first + 1 + kShortRun, hi = a.n_chunks - 1;  // last chunk that begins inside the run
-    while (lo < hi) {
-      const int mid = lo + (hi - lo + 1) / 2;
-      if (a.sorted[mid * a.chunk] == row) lo = mid;
-      else hi = mid - 1;
-    }
     Vec<VEC> s{};
     if (on) {
       if (worker == 0) s = load_vec<VEC>(a.tail + (long long)first * a.width + col);

@@ -472,16 +472,19 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
 // Blocks per matrix: 1, 2, 4 or 8; 0 where they cannot hold the matrix.  One
 // block as long as it holds all columns (4 x 128 x 256: 59 us, with two blocks
 // 74 us, the exchange costs more than half of the columns); then so many that
-// each has at most 128 (20 x 64 x 512: two blocks 53 us, four 44 us).
+// each has at most 128 (20 x 64 x 512: two blocks 53 us, four 42 us), but not
+// more than run at once, and clusters do not fill the last SMs (37 and 40 x 64 x 512:
+// two blocks 54 us, four 83 us; 58 x 96 x 764: four 139 us, eight 259 us).
+constexpr int kSmallResident = 128;
 constexpr int kSmallShared = 226 * 1024;  // of 227 KB; the rest for the kernel's own variables
 int small_columns(int n, int blocks) { return ((n + blocks - 1) / blocks + 15) / 16 * 16; }
-int small_blocks(int m, int n) {
+int small_blocks(int batch, int m, int n) {
   if (m > kSmallSide) return 0;
   int found = 0;
   for (int b = 1; b <= 8; b *= 2) {
     const int nj = small_columns(n, b);
     if (nj <= kSmallColumns && small_layout((m + 15) / 16 * 16, nj, b).bytes <= kSmallShared - 512) found = b;
-    if (found != 0 && (b == 1 || nj <= 128)) break;
+    if (found != 0 && (b == 1 || nj <= 128 || (long long)batch * 2 * b > kSmallResident)) break;
   }
   return found;
 }
@@ -495,7 +498,7 @@ cudaError_t launch_small(int batch, int rows, int cols, int steps, float scale, 
   a.tall = rows > cols;
   a.m = a.tall ? cols : rows;
   a.n = a.tall ? rows : cols;
-  const int blocks = small_blocks(a.m, a.n);
+  const int blocks = small_blocks(batch, a.m, a.n);
   a.mp = (a.m + 15) / 16 * 16;
   a.nj = small_columns(a.n, blocks);
   // Sums of like signs (the diagonal) lose half a step each time 16 columns are
@@ -1120,7 +1123,7 @@ cudaError_t launch_large(int batch, int rows, int cols, int steps, float scale, 
 
 size_t ortho_workspace(int batch, int rows, int cols) {
   const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
-  return few_rows(m, n) > 0 || small_blocks(m, n) > 0 ? 0 : pad256(large_layout(batch, m, n).bytes);
+  return few_rows(m, n) > 0 || small_blocks(batch, m, n) > 0 ? 0 : pad256(large_layout(batch, m, n).bytes);
 }
 
 cudaError_t launch_ortho(int batch, int rows, int cols, int steps, float scale, const float* g, float* out, void* ws,
@@ -1128,7 +1131,7 @@ cudaError_t launch_ortho(int batch, int rows, int cols, int steps, float scale, 
   if (batch == 0 || rows == 0 || cols == 0) return cudaSuccess;
   const int m = rows < cols ? rows : cols, n = rows < cols ? cols : rows;
   if (few_rows(m, n) > 0) return launch_few(batch, rows, cols, steps, scale, g, out, stream);
-  if (small_blocks(m, n) > 0)
+  if (small_blocks(batch, m, n) > 0)
     return launch_small(batch, rows, cols, steps, scale, g, out, stream);
   return launch_large(batch, rows, cols, steps, scale, g, out, ws, stream);
 }
