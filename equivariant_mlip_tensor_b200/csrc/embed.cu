@@ -443,10 +443,11 @@ __global__ void __launch_bounds__(kEmbedThreads, 4) embed_bwd_kernel(EmbedBwdArg
 
 // Joins the runs that cross chunk borders.  The first kJoinShort threads of a
 // block are a worker per chunk, which adds up a run that starts there and ends
-// within the next kShortRun chunks; all of the block's workers take the longer
-// ones together, one after the other, and their sums meet in shared memory in a
-// fixed order.
-constexpr int kShortRun = 4;
+// within the next short_run chunks, all side by side; all of the block's workers take the
+// longer ones together, one after the other, and their sums meet in shared memory in a
+// fixed order.  Narrow rows have more chunks in a block, and so longer queues: 200 000
+// tokens of 1 000 rows x 8 take 77 us with 4 chunks a worker, 33 with 16, 24 with 32;
+// 7 680 tokens of 16 rows x 128 8.0 with 16, 12 with 32.
 constexpr int kJoinShort = 256, kJoinLong = 1024;
 template <int VEC>
 __global__ void __launch_bounds__(kJoinLong) embed_join_kernel(EmbedBwdArgs a) {
@@ -455,6 +456,7 @@ __global__ void __launch_bounds__(kJoinLong) embed_join_kernel(EmbedBwdArgs a) {
   const int lane = threadIdx.x & (a.lpr - 1), worker = threadIdx.x / a.lpr, workers = blockDim.x / a.lpr;
   const int col = (blockIdx.y * a.lpr + lane) * VEC, chunks = kJoinShort / a.lpr;
   const bool on = col < a.width;
+  const int short_run = a.lpr >= 8 ? 16 : 32;
   const int chunk0 = blockIdx.x * chunks, chunk = chunk0 + worker;
   auto add = [](Vec<VEC>& x, const Vec<VEC>& y) {
 #pragma unroll
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(kJoinLong) embed_join_kernel(EmbedBwdArgs a) {
     const int p0 = chunk * a.chunk, p1 = p0 + a.chunk, key = a.sorted[p1 - 1];
     // the run goes on behind this chunk and starts in it
     if (a.sorted[p1] == key && (unsigned)key < (unsigned)a.n_rows && (p0 == 0 || a.sorted[p0 - 1] != key)) {
-      const int far = chunk + 1 + kShortRun;
+      const int far = chunk + 1 + short_run;
       if (far < a.n_chunks && a.sorted[far * a.chunk] == key) {
         is_long = key;
         int hi = a.n_chunks - 1;  // the last chunk that begins inside the run

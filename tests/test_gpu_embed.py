@@ -130,6 +130,22 @@ def test_long_sums_cross_many_chunks(api):
     assert np.array_equal(host(got), host(api.embed_backward(o, cuda(g))))  # the same bits again
 
 
+@pytest.mark.parametrize("width", [3, 8, 64, 128, 130])
+def test_runs_that_end_around_every_join_length(api, width):
+    """Rows whose tokens fill a given number of 16-position chunks, one less and one
+    more: joined by one worker alone, or by a block's workers together."""
+    rng = np.random.default_rng(width)
+    lengths = [16 * k + d for k in (0, 1, 2, 14, 15, 16, 17, 18, 30, 31, 32, 33, 34, 60) for d in (-1, 0, 1) if 16 * k + d >= 0]
+    rng.shuffle(lengths)
+    rows = len(lengths)
+    tok = rng.permutation(np.repeat(np.arange(rows), lengths)).astype(np.int32)
+    g = rng.standard_normal((tok.size, width)).astype(np.float32)
+    o = api.token_sort(cuda(tok), rows)
+    got = api.embed_backward(o, cuda(g), scale=0.5)
+    _check_backward(got, tok, rows, g, 0.5)
+    assert np.array_equal(host(got), host(api.embed_backward(o, cuda(g), scale=0.5)))
+
+
 def test_gradient_against_differences(api):
     """The gradient is the forward's: <embed(table + h d), g> grows by h <grad, d>."""
     rng = np.random.default_rng(4)
