@@ -563,8 +563,9 @@ int lanes_per_row(int width, int vec) {
 // does not depend on the device or on alignments).  Of the four blocks that an
 // SM holds, three are for chunks and one for the clearing, so that no block
 // starts late and runs alone at the end (200 003 x 256 of 50 021 rows: 417 + 148
-// blocks 53 us, 417 + 196 58 us; x 128: 391 + 196 33 us, 521 + 196 36 us).  At least 16
-// positions, so that the partial sums stay a small part of the reads.
+// blocks 48 us, with 417 + 196 5 us more; x 128: 391 + 196 blocks 3 us less than
+// 521 + 196).  At least 16 positions, so that the partial sums stay a small part of the
+// reads.
 int embed_chunk(int n, int width) {
   const int vec = width % 4 == 0 ? 4 : 1, lpr = lanes_per_row(width, vec);
   const long long slices = (width + lpr * vec - 1) / (lpr * vec), workers = 148LL * 3 * kEmbedThreads / lpr;
@@ -648,6 +649,7 @@ cudaError_t launch_embed_fwd(int n, int n_rows, int width, const int* tokens, co
 
 size_t embed_bwd_workspace(int n, int width) {
   const size_t chunks = ((size_t)n + embed_chunk(n, width) - 1) / embed_chunk(n, width);
+  if (chunks < 2) return 0;  // no run crosses a border
   return 2 * pad256(sizeof(float) * chunks * (size_t)width);
 }
 
@@ -663,10 +665,10 @@ static cudaError_t embed_bwd(EmbedBwdArgs a, cudaStream_t stream) {
   embed_bwd_kernel<VEC><<<(unsigned)(blocks + clear), kEmbedThreads, 0, stream>>>(a, (int)clear);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || a.n_chunks < 2) return e;
-  // large blocks where the average row crosses many chunks (20 000 tokens of 4 rows x 64: 14.6 us with
-  // blocks of 256 threads, 11.6 us with 1 024)
+  // large blocks where the average row crosses more than 128 chunks (200 000 tokens of one row x 128: 54 us with
+  // blocks of 256 threads, 33 us with 1 024; of 16 rows x 64: 20, 17; 100 000 of 50 rows x 16, 125 chunks each: 12, 15)
   const int chunks = kJoinShort / a.lpr;
-  const bool long_runs = a.n / a.n_rows > 8 * a.chunk;
+  const bool long_runs = a.n / a.n_rows > 128 * a.chunk;
   return launch_kernel(embed_join_kernel<VEC>, dim3((unsigned)((a.n_chunks - 2) / chunks + 1), (unsigned)a.slices),
                        dim3(long_runs ? kJoinLong : kJoinShort), 0, stream, true, a);
 }
