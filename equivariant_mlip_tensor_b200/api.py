@@ -254,7 +254,7 @@ def token_sort(tokens, n_rows, workspace=None):
     """Stable sort of tokens [n] into [0, n_rows) for embed_backward."""
     _check(tokens, torch.int32, "tokens")
     n, dev = tokens.numel(), tokens.device
-    order = tokens.new_empty(n)
+    order = torch.empty_like(tokens) if tokens.dim() == 1 else tokens.new_empty(n)
     srt = torch.empty_like(order)
     ws, nb = _workspace(workspace, token_sort_workspace_bytes(n, n_rows), dev)
     _call_on(dev, "cgtp_token_sort", n, n_rows, _at(tokens), _at(order), _at(srt), _at(ws), nb)
@@ -371,7 +371,7 @@ def group_norm_backward(x, gamma, beta, groups, mean, rstd, grad_y, graph_ptr=No
                  ("grad_y", grad_y), ("grad_x", grad_x))
     gg = gb = None
     if want_params:
-        gg = x.new_empty(c)
+        gg = x.new_empty(c) if gamma is None else torch.empty_like(gamma)
         gb = torch.empty_like(gg)
     ws, nb = _workspace(workspace, group_norm_workspace_bytes(n, b, c, groups, max_rows, True), dev)
     _call_on(dev, "cgtp_group_norm_backward", n, b, c, groups, _at(graph_ptr), max_rows, _at(x), stride, _at(gamma),
