@@ -551,8 +551,9 @@ cgtp_status cgtp_group_norm_backward(int n, int n_samples, int channels, int gro
 
 /* ---------------------------------------------------------------------------
  * Orthogonalised updates (an addition of this library): each matrix of a stack
- * update [batch][rows][cols] (batch <= 65535, rows and cols <= 8192), such as the gradient of the mixing matrices
- * [n_paths][mult][mult_out] that cgtp_uvw_backward returns, is brought near
+ * update [batch][rows][cols] (batch <= 65535, rows and cols <= 8192), such as
+ * the gradient of the mixing matrices [n_paths][mult][mult_out] that
+ * cgtp_uvw_backward returns, is brought near
  * the closest matrix with orthonormal rows or columns by Newton-Schulz
  * products, as the Muon optimiser does:
  *   X = G / (|G|_F + 1e-7)
