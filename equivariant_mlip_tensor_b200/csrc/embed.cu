@@ -649,7 +649,6 @@ cudaError_t launch_embed_fwd(int n, int n_rows, int width, const int* tokens, co
 
 size_t embed_bwd_workspace(int n, int width) {
   const size_t chunks = ((size_t)n + embed_chunk(n, width) - 1) / embed_chunk(n, width);
-  if (chunks < 2) return 0;  // no run crosses a border
   return 2 * pad256(sizeof(float) * chunks * (size_t)width);
 }
 
