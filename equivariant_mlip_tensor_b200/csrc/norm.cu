@@ -25,7 +25,8 @@
 //   3. each tile reads its rows again and writes the result.
 //
 // Statistics are means and sums of squared deviations from a mean, joined as
-// such, in fp32: no sum of squares that an offset could cancel.
+// such, in fp32: deviations are from the mean of their own rows or of the whole group, so no
+// sum of squares has an offset or an outlier to cancel.
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -676,32 +677,40 @@ __global__ void __launch_bounds__(kNormThreads) norm_part_kernel(NormArgs a, int
   });
 }
 
-// Sum over the TPI threads of one item, in a fixed order, valid in all of them.
-template <int TPI>
-__device__ __forceinline__ float item_sum(float v, float* red) {
+// Sums over the TPI threads of one item, in a fixed order, valid in all of them.
+template <int TPI, int K>
+__device__ __forceinline__ void item_sums(float (&v)[K], float (*red)[32]) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
   if constexpr (TPI > 32) {
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0.f;
+    if ((threadIdx.x & 31) == 0)
 #pragma unroll
-    for (int q = 0; q < TPI / 32; ++q) v += red[q];
+      for (int i = 0; i < K; ++i) red[i][threadIdx.x >> 5] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+      v[i] = 0.f;
+#pragma unroll
+      for (int q = 0; q < TPI / 32; ++q) v[i] += red[i][q];
+    }
   }
-  return v;
 }
 
 // 2: TPI threads per (sample, group) join the slots.  Forward: the mean of all
-// values, then the squared deviations from it (each part's own plus its
-// mean's); backward: the group's means of t and t h.
+// values, then, from the slots once more (they come from L2), the squared deviations from it:
+// each part's own plus its mean's.  A part may be one row that is like no other, so no part's
+// mean can stand for the whole one: squares about it would cancel.  What the mean's own
+// rounding leaves of the first moment is taken off the variance and the mean.
+// Backward: the group's means of t and t h.
 constexpr int kJoinThreads = 1024;
 template <int TPI, bool BWD>
 __global__ void __launch_bounds__(TPI > 32 ? TPI : kNormThreads)
     norm_join_kernel(NormArgs a, int rows_per_tile, const float2* __restrict__ slots, float2* __restrict__ terms) {
   grid_dependents_launch();
   grid_dependency_wait();
-  __shared__ float red[kJoinThreads / 32];
+  __shared__ float red[3][32];  // of the mean, and of the two sums
   const long long item = ((long long)blockIdx.x * blockDim.x + threadIdx.x) / TPI;
   if (item >= (long long)a.samples * a.groups) return;  // whole items leave together
   const int s = (int)(item / a.groups), g = (int)(item % a.groups), cpg = a.channels / a.groups;
@@ -712,33 +721,64 @@ __global__ void __launch_bounds__(TPI > 32 ? TPI : kNormThreads)
   const float2* base = slots + ((long long)t0 + s) * a.channels + (long long)g * cpg;
   const int tid = threadIdx.x % TPI;
   auto rows_of = [&](int t) { return min(b.y, (t + 1) * rows_per_tile) - max(b.x, t * rows_per_tile); };
-  // forward: sums of n (mean - ref) and of the deviations from ref, the first part's mean; how far the whole
-  // mean is from it is taken off at the end (part means are close: little cancels)
-  const float ref = BWD || entries == 0 ? 0.f : base[0].x;
-  float s1 = 0.f, s2 = 0.f;
+  // Every TPI-th entry, parts in order.  The forward, which takes them twice, keeps the first ones: f(rows, slot).
+  constexpr int kHeld = BWD ? 0 : 4;
+  int k = tid / cpg, c = tid % cpg;
+  const auto next = [&]() {
+    k += TPI / cpg;
+    c += TPI % cpg;
+    if (c >= cpg) {
+      c -= cpg;
+      ++k;
+    }
+  };
+  float2 held[kHeld + 1];
+  float rows[kHeld + 1];
+#pragma unroll
+  for (int i = 0; i < kHeld; ++i) {
+    const bool there = tid + (long long)i * TPI < entries;
+    held[i] = there ? base[(long long)k * a.channels + c] : make_float2(0.f, 0.f);
+    rows[i] = there ? float(rows_of(t0 + k)) : 0.f;
+    next();
+  }
+  const int k0 = k, c0 = c;
+  const auto for_slots = [&](auto&& f) {
+#pragma unroll
+    for (int i = 0; i < kHeld; ++i) f(rows[i], held[i]);
+    k = k0;
+    c = c0;
 #pragma unroll 8
-  for (long long q = tid; q < entries; q += TPI) {
-    const int k = (int)(q / cpg), c = (int)(q % cpg);
-    const float2 v = base[(long long)k * a.channels + c];
+    for (long long q = tid + kHeld * TPI; q < entries; q += TPI) {
+      f(float(rows_of(t0 + k)), base[(long long)k * a.channels + c]);
+      next();
+    }
+  };
+  float mean = 0.f, sum[2] = {};
+  if constexpr (!BWD) {
+    float all[1] = {};
+    for_slots([&](float n, float2 v) { all[0] = fmaf(n, v.x, all[0]); });
+    item_sums<TPI>(all, red + 2);
+    mean = entries > 0 ? all[0] / count : 0.f;
+  }
+  for_slots([&](float n, float2 v) {
     if constexpr (BWD) {
       const float w = a.gamma == nullptr ? 1.f : a.gamma[g * cpg + c];
-      s1 = fmaf(w, v.x, s1);
-      s2 = fmaf(w, v.y, s2);
+      sum[0] = fmaf(w, v.x, sum[0]);
+      sum[1] = fmaf(w, v.y, sum[1]);
     } else {
-      const float n = float(rows_of(t0 + k)), d = v.x - ref;
-      s1 = fmaf(n, d, s1);
-      s2 += fmaf(n * d, d, v.y);
+      const float d = v.x - mean;
+      sum[0] = fmaf(n, d, sum[0]);
+      sum[1] += fmaf(n * d, d, v.y);
     }
-  }
-  s1 = item_sum<TPI>(s1, red);
-  s2 = item_sum<TPI>(s2, red);
+  });
+  item_sums<TPI>(sum, red);
   if (tid != 0) return;
-  const float m1 = entries > 0 ? s1 / count : 0.f, m2 = entries > 0 ? s2 / count : 0.f;
+  const float m1 = entries > 0 ? sum[0] / count : 0.f, m2 = entries > 0 ? sum[1] / count : 0.f;
   if constexpr (BWD) {
     terms[item] = make_float2(m1, m2);
   } else {
     const float var = fmaf(-m1, m1, m2);
-    a.mean[item] = ref + m1;
+    a.mean[item] = mean + m1;
     a.rstd[item] = 1.f / sqrtf((var < 0.f ? 0.f : var) + a.eps);  // NaN stays
   }
 }
