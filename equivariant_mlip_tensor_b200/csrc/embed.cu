@@ -448,15 +448,19 @@ __global__ void __launch_bounds__(kEmbedThreads, 4) embed_bwd_kernel(EmbedBwdArg
 // fixed order.  Narrow rows have more chunks in a block, and so longer queues: 200 000
 // tokens of 1 000 rows x 8 take 77 us with 4 chunks a worker, 33 with 16, 24 with 32;
 // 7 680 tokens of 16 rows x 128 8.0 with 16, 12 with 32.
+// The width alone says what counts as long and over how many stripes of its chunks a long run is
+// summed: rows off a 16-byte boundary, whose workers have STRIPES = up to four times the lanes, take
+// as many stripes a worker and join them first, so that alignments change no bit (200 003 tokens of
+// 50 021 rows x 8 with an odd stride: 12 us, x 16: 15; with orders of their own 10 and 13).
 constexpr int kJoinShort = 256, kJoinLong = 1024;
-template <int VEC>
+template <int VEC, int STRIPES>
 __global__ void __launch_bounds__(kJoinLong) embed_join_kernel(EmbedBwdArgs a) {
   __shared__ Vec<VEC> part[kJoinLong];
   __shared__ int2 long_run[kJoinShort];  // by chunk of the block: the row of a long run, or -1, and its last chunk
   const int lane = threadIdx.x & (a.lpr - 1), worker = threadIdx.x / a.lpr, workers = blockDim.x / a.lpr;
   const int col = (blockIdx.y * a.lpr + lane) * VEC, chunks = kJoinShort / a.lpr;
   const bool on = col < a.width;
-  const int short_run = a.lpr >= 8 ? 16 : 32;
+  const int short_run = a.lpr >= 8 * STRIPES ? 16 : 32;
   const int chunk0 = blockIdx.x * chunks, chunk = chunk0 + worker;
   auto add = [](Vec<VEC>& x, const Vec<VEC>& y) {
 #pragma unroll
@@ -502,13 +506,21 @@ __global__ void __launch_bounds__(kJoinLong) embed_join_kernel(EmbedBwdArgs a) {
   for (int w = 0; w < chunks; ++w) {
     const int row = long_run[w].x, lo = long_run[w].y, first = chunk0 + w;
     if (row < 0) continue;  // the same for every thread
-    Vec<VEC> s{};
+    Vec<VEC> s[STRIPES] = {};
     if (on) {
-      if (worker == 0) s = load_vec<VEC>(a.tail + (long long)first * a.width + col);
+      if (worker == 0) s[0] = load_vec<VEC>(a.tail + (long long)first * a.width + col);
 #pragma unroll 4
-      for (int c = first + 1 + worker; c <= lo; c += workers) add(s, load_vec<VEC>(a.head + (long long)c * a.width + col));
+      for (int c = first + 1 + worker; c <= lo; c += STRIPES * workers)
+#pragma unroll
+        for (int i = 0; i < STRIPES; ++i)
+          if (i == 0 || c + i * workers <= lo)
+            add(s[i], load_vec<VEC>(a.head + (long long)(c + i * workers) * a.width + col));
+#pragma unroll
+      for (int o = STRIPES >> 1; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) add(s[i], s[i + o]);
     }
-    part[threadIdx.x] = s;
+    part[threadIdx.x] = s[0];
     __syncthreads();
     for (int o = workers >> 1; o > 0; o >>= 1) {
       if (worker < o) add(part[threadIdx.x], part[threadIdx.x + o * a.lpr]);
@@ -559,6 +571,9 @@ int lanes_per_row(int width, int vec) {
   while (l < 32 && l < need) l <<= 1;
   return l;
 }
+// Lanes of a row on a 16-byte boundary, by the width alone.
+int order_lanes(int width) { return lanes_per_row(width, width % 4 == 0 ? 4 : 1); }
+
 // Sorted positions per chunk, a function of the sizes alone (the sums' order
 // does not depend on the device or on alignments).  Of the four blocks that an
 // SM holds, three are for chunks and one for the clearing, so that no block
@@ -567,7 +582,7 @@ int lanes_per_row(int width, int vec) {
 // 521 + 196).  At least 16 positions, so that the partial sums stay a small part of the
 // reads.
 int embed_chunk(int n, int width) {
-  const int vec = width % 4 == 0 ? 4 : 1, lpr = lanes_per_row(width, vec);
+  const int vec = width % 4 == 0 ? 4 : 1, lpr = order_lanes(width);
   const long long slices = (width + lpr * vec - 1) / (lpr * vec), workers = 148LL * 3 * kEmbedThreads / lpr;
   const long long c = ((n * slices + workers - 1) / workers + 7) / 8 * 8;
   return c < 16 ? 16 : c > 256 ? 256 : (int)c;
@@ -668,7 +683,11 @@ static cudaError_t embed_bwd(EmbedBwdArgs a, cudaStream_t stream) {
   // blocks of 256 threads, 33 us with 1 024; of 16 rows x 64: 20, 17; 100 000 of 50 rows x 16, 125 chunks each: 12, 15)
   const int chunks = kJoinShort / a.lpr;
   const bool long_runs = a.n / a.n_rows > 128 * a.chunk;
-  return launch_kernel(embed_join_kernel<VEC>, dim3((unsigned)((a.n_chunks - 2) / chunks + 1), (unsigned)a.slices),
+  const int stripes = a.lpr / order_lanes(a.width);
+  const auto join = VEC == 4 || stripes == 1 ? embed_join_kernel<VEC, 1>
+                    : stripes == 2           ? embed_join_kernel<1, 2>
+                                             : embed_join_kernel<1, 4>;
+  return launch_kernel(join, dim3((unsigned)((a.n_chunks - 2) / chunks + 1), (unsigned)a.slices),
                        dim3(long_runs ? kJoinLong : kJoinShort), 0, stream, true, a);
 }
 

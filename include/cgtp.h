@@ -488,9 +488,10 @@ cgtp_status cgtp_cp_backward(cgtp_plan plan, int rank, int batch, const float* A
  * of the size cgtp_token_sort_workspace_size reports.
  * cgtp_embed_backward: order and sorted as cgtp_token_sort wrote them for the
  * same n_rows.  Every row of grad_table is overwritten (zero for a row without
- * tokens).  The sums run in the order of the sort, cut into chunks by n and
- * width alone: equal inputs give equal bits.  Entries of order and sorted that
- * are out of range are left out, never followed.
+ * tokens).  The sums run in the order of the sort, cut and joined by n, n_rows
+ * and width alone: equal values give equal bits, whatever the strides and
+ * alignments of their rows.  Entries of order and sorted that are out of range
+ * are left out, never followed.
  * ------------------------------------------------------------------------- */
 cgtp_status cgtp_token_sort_workspace_size(int n, int n_rows, size_t* bytes);
 cgtp_status cgtp_token_sort(int n, int n_rows, const int* tokens, int* order, int* sorted,
