@@ -476,14 +476,14 @@ __global__ void __launch_bounds__(kSmallThreads + 32, 1) ortho_small_kernel(Smal
 // more than run at once, and clusters do not fill the last SMs (37 and 40 x 64 x 512:
 // two blocks 54 us, four 83 us; 58 x 96 x 764: four 139 us, eight 259 us).
 constexpr int kSmallResident = 128;
-constexpr int kSmallShared = 226 * 1024;  // of 227 KB; the rest for the kernel's own variables
+constexpr int kSmallShared = 226 * 1024 - 512;  // of 227 KB; the rest for the kernel's own variables
 int small_columns(int n, int blocks) { return ((n + blocks - 1) / blocks + 15) / 16 * 16; }
 int small_blocks(int batch, int m, int n) {
   if (m > kSmallSide) return 0;
   int found = 0;
   for (int b = 1; b <= 8; b *= 2) {
     const int nj = small_columns(n, b);
-    if (nj <= kSmallColumns && small_layout((m + 15) / 16 * 16, nj, b).bytes <= kSmallShared - 512) found = b;
+    if (nj <= kSmallColumns && small_layout((m + 15) / 16 * 16, nj, b).bytes <= kSmallShared) found = b;
     if (found != 0 && (b == 1 || nj <= 128 || (long long)batch * 2 * b > kSmallResident)) break;
   }
   return found;
@@ -511,7 +511,9 @@ cudaError_t launch_small(int batch, int rows, int cols, int steps, float scale, 
   a.g = g;
   a.out = out;
   const int bytes = small_layout(a.mp, a.nj, blocks).bytes;
-  cudaError_t e = cudaFuncSetAttribute(ortho_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  // the limit belongs to the kernel, not to the call: always the same one, so that no thread takes from
+  // another what it is about to launch with
+  cudaError_t e = cudaFuncSetAttribute(ortho_small_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmallShared);
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)batch * blocks);
@@ -712,8 +714,9 @@ cudaError_t launch_few(int batch, int rows, int cols, int steps, float scale, co
                                         : kp == 8  ? ortho_few_kernel<8>
                                         : kp == 16 ? ortho_few_kernel<16>
                                                    : ortho_few_kernel<32>;
-  if (L.bytes > 48 * 1024) {  // more than a block gets unasked
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, L.bytes);
+  if (L.bytes > 48 * 1024) {  // more than a block gets unasked: what the longest rows of the kernel take
+    const int most = few_layout(kp, kFewWork / (kp * kp)).bytes;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
   }
   kernel<<<batch, threads, L.bytes, stream>>>(a, shift(L.quads), shift(kp / 4));
