@@ -119,8 +119,9 @@ __device__ __forceinline__ Vec<VEC> all(float s) {
   return r;
 }
 
-// 1 / (1 + exp(-z)) by the hardware's base-2 exponential and reciprocal: off by
-// some (|z| + 3) 2^-24 (1 - s) of itself, and 0 or 1 at the ends.
+// 1 / (1 + exp(-z)) by the hardware's base-2 exponential and reciprocal, and 0 or 1
+// at the ends.  The exponential is off by some (|z| + 3) 2^-24 of itself, of which 1 - s
+// reaches s; the sum 1 + e and the reciprocal add some 3 x 2^-24 wherever z lies.
 __device__ __forceinline__ float sigmoid(float z) {
   float e, s;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(z * -1.4426950408889634f));

@@ -532,7 +532,9 @@ typedef enum { CGTP_ACT_NONE = 0, CGTP_ACT_SILU = 1 } cgtp_act;
  * direction (0 bytes where none is needed; NULL is accepted then).
  *
  * Backward: grad_x (nullable), grad_gamma and grad_beta ([channels], nullable),
- * all overwritten; x, gamma, beta, mean, rstd as in the forward.
+ * all overwritten; x, gamma, beta, mean, rstd as in the forward.  There is no
+ * adjoint of it (no counterpart of cgtp_conv_double_backward), so forces that go
+ * through a norm cannot be trained on by this library alone.
  * ------------------------------------------------------------------------- */
 cgtp_status cgtp_group_norm_workspace_size(int n, int n_samples, int channels, int groups,
                                            int max_rows, int backward, size_t* bytes);
